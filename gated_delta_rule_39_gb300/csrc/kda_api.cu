@@ -7,19 +7,21 @@
 #include <mutex>
 #include <vector>
 
-#include "kda_internal.cuh"
+#include "kda_host.cuh"
 
 namespace kda {
 namespace {
-
 // cudaError_t behind the calling thread's most recent KDA_ERR_LAUNCH / ALLOC / CUDA
 thread_local int t_last_cuda_error = 0;
-// record a CUDA failure, clear the runtime's (non-sticky) last error, pass `status` on
+}  // namespace
+
 int cuda_fail(int status, cudaError_t e) {
     t_last_cuda_error = static_cast<int>(e);
     cudaGetLastError();
     return status;
 }
+
+namespace {
 
 // Device-side error word (one per device: every device that loads the module
 // holds its own instance).  Kernels receive its address.
@@ -40,8 +42,9 @@ struct DeviceInfo {
 };
 DeviceInfo g_dev[kMaxDevices];
 std::mutex g_dev_mu;
+}  // namespace
 
-int device_setup(int* dev_out, int** err_out, int* sms_out = nullptr) {
+int device_setup(int* dev_out, int** err_out, int* sms_out) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return cuda_fail(KDA_ERR_CUDA, e);
@@ -75,6 +78,7 @@ int device_setup(int* dev_out, int** err_out, int* sms_out = nullptr) {
     return d.arch_ok ? KDA_OK : KDA_ERR_ARCH;
 }
 
+namespace {
 // ---- launch timing ------------------------------------------------------------
 struct TimingRecord {
     int kernel;
@@ -100,32 +104,25 @@ cudaEvent_t prof_event() {
     return e;
 }
 
-template <class F>
-cudaError_t timed_launch(int kernel, cudaStream_t s, F&& launch) {
-    bool on;
-    {
-        std::lock_guard<std::mutex> lk(g_prof.mu);
-        on = g_prof.on;
-    }
-    if (!on) return launch();
-    cudaEvent_t a, b;
-    {
-        std::lock_guard<std::mutex> lk(g_prof.mu);
-        a = prof_event();
-        b = prof_event();
-    }
-    cudaEventRecord(a, s);
-    cudaError_t e = launch();
-    cudaEventRecord(b, s);
+}  // namespace
+
+LaunchTimer::LaunchTimer(int kernel, cudaStream_t s) : kernel_(kernel), stream_(s) {
     std::lock_guard<std::mutex> lk(g_prof.mu);
-    g_prof.pending.push_back({kernel, a, b});
-    return e;
+    if (!g_prof.on) return;
+    start_ = prof_event();
+    stop_ = prof_event();
+    cudaEventRecord(start_, stream_);
 }
 
-// ---- scratch ------------------------------------------------------------------
-constexpr size_t kAlign = 256;
-inline size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
+LaunchTimer::~LaunchTimer() {
+    if (!start_) return;
+    cudaEventRecord(stop_, stream_);
+    std::lock_guard<std::mutex> lk(g_prof.mu);
+    g_prof.pending.push_back({kernel_, start_, stop_});
+}
 
+namespace {
+// ---- scratch ------------------------------------------------------------------
 // Scratch of one call: the varlen sequence map (longest-first order, valid flag and
 // the unit counter of a persistent launch); fixed-length calls need none unless they
 // are split into segments.
@@ -179,12 +176,6 @@ SplitScratch split_layout(int N, int H, int s) {
     return L;
 }
 size_t split_bytes(int N, int H, int s) { return split_layout(N, H, s).total; }
-
-bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
-    if (!a || !b || na == 0 || nb == 0) return false;
-    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-    return x < y + nb && y < x + na;
-}
 
 // Host-side checks shared by kda_fwd and kda_fwd_host; no CUDA call.
 int validate(const void* q, const void* k, const void* v, const void* g, const void* beta,
@@ -482,6 +473,8 @@ const char* kda_status_string(int status) {
         case KDA_ERR_SCRATCH_LIMIT:
             return "KDA_ERR_SCRATCH_LIMIT: kda_fwd_noalloc takes at most KDA_NOALLOC_MAX_SEQS "
                    "(65536) sequences";
+        case KDA_ERR_BAD_INDEX:
+            return "KDA_ERR_BAD_INDEX: a position, slot, length or token is out of range";
         default: return "unknown kda_status";
     }
 }
@@ -935,6 +928,11 @@ const char* kda_kernel_name(int kernel_id) {
         case KDA_KERNEL_BWD: return "bwd_kernel";
         case KDA_KERNEL_BWD_FINISH: return "bwd_finish_kernel";
         case KDA_KERNEL_BWD_REDUCE: return "bwd_reduce_kernel";
+        case KDA_KERNEL_QK_NORM: return "qk_norm_kernel";
+        case KDA_KERNEL_QK_NORM_BWD: return "qk_norm_bwd_kernel";
+        case KDA_KERNEL_QK_NORM_DW: return "qk_norm_dw_kernel";
+        case KDA_KERNEL_VERIFY: return "verify_kernel";
+        case KDA_KERNEL_GDR_STEP: return "gdr_step_kernel";
         default: return "unknown";
     }
 }

@@ -1,0 +1,171 @@
+// The C entry points of the gated delta rule with one decay per value head: checks,
+// scratch and launches (the operation and its kernels: kda_gdr.cuh).
+#include <algorithm>
+#include <cmath>
+
+#include "kda_gdr.cuh"
+
+namespace kda {
+
+size_t gdr_span(long long tokens, int heads, long long stride) {
+    return tokens ? ((size_t)(tokens - 1) * stride + (size_t)heads * kDim) * 2 : 0;
+}
+
+int gdr_validate(const GdrInputs& in, int B, int K, int V, const void* s0, int s0_dtype, const void* s1,
+                 int s1_dtype, long long pool) {
+    if (K != kDim || V != kDim) return KDA_ERR_UNSUPPORTED_DIM;
+    if (B < 0 || in.T < 0 || in.Hk < 1 || in.Hv < 1 || in.Hv % in.Hk) return KDA_ERR_SHAPE;
+    const long long tok = (long long)B * in.T;
+    if (tok >= (1LL << 31) || tok * in.Hv * kDim >= (1LL << 40)) return KDA_ERR_SHAPE;
+    if (pool < 0 || pool * in.Hv >= (1LL << 31) / 2) return KDA_ERR_SHAPE;
+    if (tok > 0 && (!in.q || !in.k || !in.v || !in.g || !in.beta)) return KDA_ERR_NULL;
+    if (in.gate_dtype != KDA_BF16 && in.gate_dtype != KDA_F32) return KDA_ERR_DTYPE;
+    if (s0 && s0_dtype != KDA_BF16 && s0_dtype != KDA_F32) return KDA_ERR_DTYPE;
+    if (s1 && s1_dtype != KDA_BF16 && s1_dtype != KDA_F32) return KDA_ERR_DTYPE;
+    if (!std::isfinite(in.scale)) return KDA_ERR_ARG;
+    if (in.q_stride < (long long)in.Hk * kDim || in.k_stride < (long long)in.Hk * kDim ||
+        in.v_stride < (long long)in.Hv * kDim)
+        return KDA_ERR_SHAPE;
+    if (in.q_stride % 8 || in.k_stride % 8 || in.v_stride % 8) return KDA_ERR_ALIGN;
+    for (const void* p : {static_cast<const void*>(in.q), static_cast<const void*>(in.k),
+                          static_cast<const void*>(in.v), s0, s1})
+        if (!aligned16(p)) return KDA_ERR_ALIGN;
+    const size_t gate = in.gate_dtype == KDA_F32 ? 4 : 2;
+    for (const void* p : {in.g, in.beta})
+        if (reinterpret_cast<uintptr_t>(p) % gate) return KDA_ERR_ALIGN;
+    return KDA_OK;
+}
+
+namespace {
+
+size_t state_bytes(long long count, int Hv, int dtype) {
+    return (size_t)count * Hv * kDim * kDim * (dtype == KDA_F32 ? 4 : 2);
+}
+
+// Whether [p, p + n) overlaps an input of the rule.
+bool hits_inputs(const GdrInputs& in, long long tok, const void* p, size_t n) {
+    const size_t gates = (size_t)tok * in.Hv * (in.gate_dtype == KDA_F32 ? 4 : 2);
+    return overlaps(p, n, in.q, gdr_span(tok, in.Hk, in.q_stride)) ||
+           overlaps(p, n, in.k, gdr_span(tok, in.Hk, in.k_stride)) ||
+           overlaps(p, n, in.v, gdr_span(tok, in.Hv, in.v_stride)) || overlaps(p, n, in.g, gates) ||
+           overlaps(p, n, in.beta, gates);
+}
+
+bool states_clash(const void* s0, size_t n0, int d0, const void* s1, size_t n1, int d1) {
+    return overlaps(s0, n0, s1, n1) && (s0 != s1 || d0 != d1);
+}
+
+}  // namespace
+}  // namespace kda
+
+using namespace kda;
+
+extern "C" {
+
+int kda_gdr_step(const void* q, const void* k, const void* v, const void* g, const void* beta,
+                 int gate_dtype, float scale, void* out, const void* state_in, int state_in_dtype,
+                 void* state_out, int state_out_dtype, const int32_t* slots, int num_slots,
+                 const int32_t* lengths, int N, int T, int Hk, int Hv, int K, int V,
+                 long long q_stride, long long k_stride, long long v_stride, void* stream) {
+    GdrStep P{};
+    P.in = {static_cast<const __nv_bfloat16*>(q), static_cast<const __nv_bfloat16*>(k),
+            static_cast<const __nv_bfloat16*>(v), q_stride, k_stride, v_stride, g, beta, gate_dtype,
+            scale, nullptr, nullptr, N, T, Hk, Hv};
+    const long long pool = slots ? num_slots : N;
+    int rc = gdr_validate(P.in, N, K, V, state_in, state_in_dtype, state_out, state_out_dtype,
+                          std::max<long long>(pool, N));
+    if (rc != KDA_OK) return rc;
+    if (slots && num_slots < 1) return KDA_ERR_SHAPE;
+    if (!aligned16(out)) return KDA_ERR_ALIGN;
+    for (const int32_t* p : {slots, lengths})
+        if (reinterpret_cast<uintptr_t>(p) % 4) return KDA_ERR_ALIGN;
+    const long long tok = (long long)N * T;
+    const size_t n_out = (size_t)tok * Hv * kDim * 2, n_ids = (size_t)N * 4;
+    const size_t n_in = state_bytes(pool, Hv, state_in_dtype), n_so = state_bytes(pool, Hv, state_out_dtype);
+    if (hits_inputs(P.in, tok, out, n_out) || hits_inputs(P.in, tok, state_out, n_so) ||
+        overlaps(out, n_out, state_in, n_in) || overlaps(out, n_out, state_out, n_so) ||
+        states_clash(state_in, n_in, state_in_dtype, state_out, n_so, state_out_dtype))
+        return KDA_ERR_ALIAS;
+    for (const int32_t* p : {slots, lengths})
+        if (overlaps(out, n_out, p, n_ids) || overlaps(state_out, n_so, p, n_ids)) return KDA_ERR_ALIAS;
+    int dev = 0;
+    int* err = nullptr;
+    rc = device_setup(&dev, &err);
+    if (rc != KDA_OK) return rc;
+    P.out = static_cast<__nv_bfloat16*>(out);
+    P.state_in = state_in;
+    P.in_dtype = state_in_dtype;
+    P.state_out = state_out;
+    P.out_dtype = state_out_dtype;
+    P.slots = slots;
+    P.lengths = lengths;
+    P.pool = (int)pool;
+    P.err = err;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const cudaError_t e = timed_launch(KDA_KERNEL_GDR_STEP, s, [&] { return launch_gdr_step(P, s); });
+    if (e != cudaSuccess) return cuda_fail(KDA_ERR_LAUNCH, e);
+    return KDA_OK;
+}
+
+int kda_gdr_fwd(const void* q, const void* k, const void* v, const void* g, const void* beta,
+                int gate_dtype, float scale, void* out, const void* initial_state,
+                int initial_state_dtype, void* final_state, int final_state_dtype,
+                const int32_t* cu_seqlens, int num_seqs, int B, int T, int Hk, int Hv, int K, int V,
+                long long q_stride, long long k_stride, long long v_stride, void* stream) {
+    const bool varlen = cu_seqlens != nullptr;
+    const int N = varlen ? num_seqs : B;
+    GdrStep P{};
+    P.in = {static_cast<const __nv_bfloat16*>(q), static_cast<const __nv_bfloat16*>(k),
+            static_cast<const __nv_bfloat16*>(v), q_stride, k_stride, v_stride, g, beta, gate_dtype,
+            scale, cu_seqlens, nullptr, N, T, Hk, Hv};
+    if (B < 1 || (varlen && (B != 1 || num_seqs < 1))) return KDA_ERR_SHAPE;
+    int rc = gdr_validate(P.in, B, K, V, initial_state, initial_state_dtype, final_state,
+                          final_state_dtype, N);
+    if (rc != KDA_OK) return rc;
+    const long long tok = (long long)B * T;
+    if (tok > 0 && !out) return KDA_ERR_NULL;
+    if (!aligned16(out) || reinterpret_cast<uintptr_t>(cu_seqlens) % 4) return KDA_ERR_ALIGN;
+    const size_t n_out = (size_t)tok * Hv * kDim * 2;
+    const size_t n_in = state_bytes(N, Hv, initial_state_dtype), n_so = state_bytes(N, Hv, final_state_dtype);
+    if (hits_inputs(P.in, tok, out, n_out) || hits_inputs(P.in, tok, final_state, n_so) ||
+        overlaps(out, n_out, initial_state, n_in) || overlaps(out, n_out, final_state, n_so) ||
+        states_clash(initial_state, n_in, initial_state_dtype, final_state, n_so, final_state_dtype) ||
+        overlaps(out, n_out, cu_seqlens, ((size_t)N + 1) * 4) ||
+        overlaps(final_state, n_so, cu_seqlens, ((size_t)N + 1) * 4))
+        return KDA_ERR_ALIAS;
+    int dev = 0;
+    int* err = nullptr;
+    rc = device_setup(&dev, &err);
+    if (rc != KDA_OK) return rc;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    int* scratch = nullptr;
+    cudaError_t e = cudaSuccess;
+    if (varlen) {
+        e = cudaMallocAsync(reinterpret_cast<void**>(&scratch), align_up(((size_t)N + 2) * 4), s);
+        if (e != cudaSuccess) return cuda_fail(KDA_ERR_ALLOC, e);
+        Problem FP{};
+        FP.cu_seqlens = cu_seqlens;
+        FP.N = N;
+        FP.T = T;
+        FP.H = Hv;
+        SeqMap M{};
+        M.seq_order = scratch;
+        M.valid = scratch + N;
+        P.in.valid = M.valid;
+        e = timed_launch(KDA_KERNEL_SEQMAP, s, [&] { return launch_seqmap(FP, M, err, s); });
+    }
+    P.out = static_cast<__nv_bfloat16*>(out);
+    P.state_in = initial_state;
+    P.in_dtype = initial_state_dtype;
+    P.state_out = final_state;
+    P.out_dtype = final_state_dtype;
+    P.pool = N;
+    P.err = err;
+    if (e == cudaSuccess)
+        e = timed_launch(KDA_KERNEL_GDR_STEP, s, [&] { return launch_gdr_step(P, s); });
+    if (scratch) cudaFreeAsync(scratch, s);
+    if (e != cudaSuccess) return cuda_fail(KDA_ERR_LAUNCH, e);
+    return KDA_OK;
+}
+
+}  // extern "C"

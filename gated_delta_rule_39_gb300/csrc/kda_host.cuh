@@ -1,0 +1,50 @@
+// Host-side helpers shared by the C ABI's translation units (defined in kda_api.cu).
+#pragma once
+#include <cstddef>
+#include <cstdint>
+
+#include "kda_internal.cuh"
+
+namespace kda {
+
+// Record a CUDA failure for kda_last_cuda_error, clear the runtime's (non-sticky) last
+// error, pass `status` on.
+int cuda_fail(int status, cudaError_t e);
+
+// The current device, its error word and its SM count; KDA_ERR_ARCH if it is not a
+// compute capability 10.3 GPU.  Set up once per device.
+int device_setup(int* dev_out, int** err_out, int* sms_out = nullptr);
+
+// Records the launches between its construction and its destruction, with their device
+// time, under a kernel id (kda_profile_*); nothing while recording is off.
+class LaunchTimer {
+public:
+    LaunchTimer(int kernel, cudaStream_t s);
+    ~LaunchTimer();
+    LaunchTimer(const LaunchTimer&) = delete;
+    LaunchTimer& operator=(const LaunchTimer&) = delete;
+
+private:
+    int kernel_;
+    cudaStream_t stream_;
+    cudaEvent_t start_ = nullptr, stop_ = nullptr;
+};
+
+template <class F>
+cudaError_t timed_launch(int kernel, cudaStream_t s, F&& launch) {
+    LaunchTimer timer(kernel, s);
+    return launch();
+}
+
+constexpr size_t kAlign = 256;
+inline size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
+
+inline bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
+    if (!a || !b || na == 0 || nb == 0) return false;
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y + nb && y < x + na;
+}
+
+inline bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+
+}  // namespace kda

@@ -63,8 +63,12 @@ typedef enum {
     KDA_ERR_ARG = -12,            /* scale or lower_bound outside the supported range  */
     KDA_ERR_ALIAS = -13,          /* out overlaps an input, or states alias unsafely   */
     KDA_ERR_SCRATCH_LIMIT = -14,  /* kda_fwd_noalloc: num_seqs > KDA_NOALLOC_MAX_SEQS   */
-    KDA_ERR_SEGMENTS = -15        /* kda_fwd_segments: num_segments not possible       */
+    KDA_ERR_SEGMENTS = -15,       /* kda_fwd_segments: num_segments not possible       */
+    KDA_ERR_BAD_INDEX = -16       /* a position, slot, length or token out of range (device) */
 } kda_status;
+
+/* The norm of kda_qk_norm: x / sqrt(sum x^2 + eps), or x / sqrt(mean x^2 + eps). */
+typedef enum { KDA_NORM_L2 = 0, KDA_NORM_RMS = 1 } kda_norm;
 
 /*
  * kda_fwd -- KDA forward (prefill) pass.
@@ -233,7 +237,7 @@ size_t kda_bwd_workspace_bytes(int B, int T, int H, int num_seqs, int varlen);
 
 /*
  * kda_fwd_get_error -- synchronise `stream`, then return and clear the current
- * device's error word: KDA_OK, KDA_ERR_BAD_SEQLENS or KDA_ERR_DEVICE_TIMEOUT
+ * device's error word: KDA_OK, KDA_ERR_BAD_SEQLENS, KDA_ERR_BAD_INDEX or KDA_ERR_DEVICE_TIMEOUT
  * (or KDA_ERR_CUDA if the synchronisation itself failed).  There is one word
  * per device, shared by every call on it whatever its stream: it keeps the
  * first error any kernel recorded since the last read, and a call still
@@ -327,10 +331,145 @@ int kda_decode(const void* q, const void* k, const void* v, const void* g, const
                float lower_bound, const void* state_in, int state_in_dtype, void* state_out,
                int state_out_dtype, int N, int H, int K, int V, void* stream);
 
+/* ---- the gated delta rule with one decay per head, and what a model runs around it --
+ *
+ * The entry points below serve models whose delta rule has one decay per head:
+ *
+ *   S' = e^(g_t) S,  d = beta_t (v_t - S'^T k_t),  S = S' + k_t d^T,  o_t = scale S^T q_t
+ *
+ * with g (the log of the decay, at most 0 in use; -inf forgets the state) and beta
+ * (the write strength) given as they are: no activation is applied inside, and g
+ * has no lower bound.  Hv value heads share Hk <= Hv query and key heads in groups of
+ * Hv / Hk neighbours: value head h reads the queries and keys of head h / (Hv / Hk).
+ *
+ *   prompt    kda_qk_norm -> kda_gdr_fwd
+ *   decoding  kda_qk_norm -> kda_gdr_step (outputs of the drafted tokens) -> the model's
+ *             head -> kda_verify_drafts -> kda_gdr_step (states after the kept tokens)
+ *   training  kda_qk_norm -> kda_gdr_fwd; kda_gdr_bwd -> kda_qk_norm_bwd
+ *
+ * They follow the same rules as the calls above: device pointers owned by the caller,
+ * asynchronous on `stream`, argument errors returned before anything is launched or
+ * written.  Indices that only the device can check (positions, slots, lengths, tokens)
+ * set KDA_ERR_BAD_INDEX in the error word, and what they belong to is not written.
+ */
+
+/*
+ * kda_qk_norm -- norms of queries and keys for each head, with the position rotation in
+ * the same pass:  y = w x / sqrt(c sum x^2 + eps), c = 1 (KDA_NORM_L2) or 1 / D
+ * (KDA_NORM_RMS), and its first rotary_dim channels turned in pairs by the token's angles:
+ * (y_a cos - y_b sin, y_b cos + y_a sin).
+ *
+ *   q, k        [T, Hq, D] and [T, Hk, D] of dtype (KDA_BF16 or KDA_F32); D even, at most
+ *               512 (KDA_ERR_UNSUPPORTED_DIM); the D channels of a head and the heads of
+ *               a token are contiguous, tokens are q_stride / k_stride elements apart
+ *               (so both may be views of the buffer of one projection); Hk = 0: no keys
+ *   q_out, k_out  [T, Hq, D] and [T, Hk, D] of dtype, contiguous; in place where the
+ *               input is contiguous too
+ *   eps         finite, at least 0; a row of zeros gives zeros with eps > 0
+ *   q_weight, k_weight  fp32 [D] or NULL (ones)
+ *   cos, sin    fp32 [table_rows, rotary_dim / 2], unused when rotary_dim is 0
+ *   positions   int32 [T], the table row of each token, or NULL (token t uses row t); a
+ *               position outside the table sets KDA_ERR_BAD_INDEX and that token's rows are
+ *               not written
+ *   interleaved 0: channel i pairs with i + rotary_dim / 2; else 2 i with 2 i + 1
+ *
+ * Arithmetic is fp32, rounded once on the store.  Any element alignment and stride is
+ * accepted; 16-byte aligned rows with rotary_dim / 2 a multiple of 8 (bf16) or 4 (fp32)
+ * run with 16-byte accesses.
+ */
+int kda_qk_norm(const void* q, const void* k, void* q_out, void* k_out, int dtype, int norm,
+                float eps, const float* q_weight, const float* k_weight, const float* cos,
+                const float* sin, const int32_t* positions, int table_rows, int rotary_dim,
+                int interleaved, int T, int Hq, int Hk, int D, long long q_stride,
+                long long k_stride, void* stream);
+
+/*
+ * kda_qk_norm_bwd -- its backward pass, from the inputs alone (the norms are formed again).
+ *   dq_out, dk_out  dL/d(q_out), dL/d(k_out): [T, Hq, D], [T, Hk, D] of dtype, contiguous
+ *   dq, dk          dL/dq, dL/dk of dtype, contiguous
+ *   dq_weight, dk_weight  fp32 [D], required with the weight and NULL without it; summed
+ *               over tokens and heads in a fixed order (results are deterministic)
+ * Other arguments as kda_qk_norm.  With weights it takes a few hundred KB of scratch from the
+ * stream-ordered allocator.
+ */
+int kda_qk_norm_bwd(const void* q, const void* k, const void* dq_out, const void* dk_out, void* dq,
+                    void* dk, int dtype, int norm, float eps, const float* q_weight,
+                    const float* k_weight, float* dq_weight, float* dk_weight, const float* cos,
+                    const float* sin, const int32_t* positions, int table_rows, int rotary_dim,
+                    int interleaved, int T, int Hq, int Hk, int D, long long q_stride,
+                    long long k_stride, void* stream);
+
+/*
+ * kda_gdr_fwd -- the rule over whole sequences (prefill, training).
+ *
+ *   q, k        bf16 [B, T, Hk, 128], used as given (kda_qk_norm normalises them)
+ *   v, out      bf16 [B, T, Hv, 128]; Hv a multiple of Hk
+ *   q_stride, k_stride, v_stride   elements from one token to the next (the B * T tokens
+ *               are equally spaced), multiples of 8; heads and channels are contiguous, and
+ *               so is out
+ *   g, beta     [B, T, Hv] of gate_dtype (KDA_BF16 or KDA_F32)
+ *   initial_state, final_state, cu_seqlens, num_seqs   as kda_fwd: [N, Hv, 128, 128], row =
+ *               key channel, or NULL; a malformed cu_seqlens writes nothing
+ *   B >= 1, T >= 0, K = V = 128
+ */
+int kda_gdr_fwd(const void* q, const void* k, const void* v, const void* g, const void* beta,
+                int gate_dtype, float scale, void* out, const void* initial_state,
+                int initial_state_dtype, void* final_state, int final_state_dtype,
+                const int32_t* cu_seqlens, int num_seqs, int B, int T, int Hk, int Hv, int K, int V,
+                long long q_stride, long long k_stride, long long v_stride, void* stream);
+
+/*
+ * kda_gdr_step -- the rule for T new tokens (one, or a few drafted ones) of each of N
+ * sequences, on states held in memory.  All arithmetic is fp32.
+ *
+ *   q, k        bf16 [N, T, Hk, 128]; v, out bf16 [N, T, Hv, 128]; g, beta [N, T, Hv];
+ *               strides as kda_gdr_fwd.  out may be NULL (only the states advance)
+ *   state_in    NULL (zero states) or a pool [num_slots, Hv, 128, 128]
+ *   state_out   NULL (nothing kept) or such a pool; the same buffer as state_in updates it
+ *               in place
+ *   slots       int32 [N], the state of each sequence in both pools (distinct ones), -1 for
+ *               a padding entry that is neither read nor written; NULL: sequence n uses
+ *               state n and the pools hold N states (num_slots is not read)
+ *   lengths     int32 [N] in 0 .. T or NULL (T): out has all T tokens, state_out the state
+ *               after the first lengths[n] of them.  After kda_verify_drafts a second call
+ *               with out = NULL and lengths = the tokens to keep advances the states without
+ *               a copy of any of them per drafted token
+ * A slot or length out of range sets KDA_ERR_BAD_INDEX and writes nothing of its sequence.
+ */
+int kda_gdr_step(const void* q, const void* k, const void* v, const void* g, const void* beta,
+                 int gate_dtype, float scale, void* out, const void* state_in, int state_in_dtype,
+                 void* state_out, int state_out_dtype, const int32_t* slots, int num_slots,
+                 const int32_t* lengths, int N, int T, int Hk, int Hv, int K, int V,
+                 long long q_stride, long long k_stride, long long v_stride, void* stream);
+
+/*
+ * kda_verify_drafts -- verification of drafted tokens against the target's probabilities,
+ * from random numbers that the caller draws.  Draft i, token x_i, is kept while
+ * uniform_i q_i(x_i) < p_i(x_i); after the first that is not kept, at place a, the next token
+ * is argmax_v max(p_a(v) - q_a(v), 0) / noise(v), or argmax_v p_a(v) / noise(v) where nothing
+ * is left of p_a or every draft was kept.  With noise ~ Exp(1) that draws from the
+ * distribution in the numerator, so the tokens follow the target's own distribution.
+ * Ties go to the lowest index; what is not above 0 (NaN included) is never chosen.
+ *
+ *   target_probs  [N, D + 1, V] of dtype (KDA_F32 or KDA_BF16)
+ *   draft_probs   [N, D, V] of dtype, or NULL: the drafts were certain (q_i(x_i) = 1)
+ *   draft_tokens  int32 [N, D]        uniform  fp32 [N, D] in [0, 1)
+ *   noise         fp32 [N, V], above 0
+ *   num_drafts    int32 [N] in 0 .. D, or NULL (D)
+ *   accepted      int32 [N]: drafts kept
+ *   tokens        int32 [N, D + 1]: the kept drafts, the next token, then -1 (-1 in the next
+ *                 token's place too if the row has nothing above 0)
+ * A count or token out of range sets KDA_ERR_BAD_INDEX and writes nothing of its sequence.
+ */
+int kda_verify_drafts(const void* target_probs, const void* draft_probs, int dtype,
+                      const int32_t* draft_tokens, const float* uniform, const float* noise,
+                      const int32_t* num_drafts, int32_t* accepted, int32_t* tokens, int N, int D,
+                      int V, void* stream);
+
 /* ---- launch accounting (for measurement; off by default) ------------------
  *
- * kda_profile_enable(1) makes every later kda_fwd, kda_fwd_noalloc and
- * kda_decode call (and the kda_fwd calls that kda_fwd_host makes) record a CUDA
+ * kda_profile_enable(1) makes every later call that launches kernels
+ * (and the kda_fwd calls that kda_fwd_host makes) record a CUDA
  * event before and after each of its kernel launches, on the launch stream; enable(0)
  * stops recording.  Enabling clears the totals.  kda_profile_read
  * synchronises on the recorded events and returns, per kernel id
@@ -347,7 +486,12 @@ enum {
     KDA_KERNEL_BWD = 6,
     KDA_KERNEL_BWD_FINISH = 7,
     KDA_KERNEL_BWD_REDUCE = 8,
-    KDA_NUM_KERNELS = 9
+    KDA_KERNEL_QK_NORM = 9,
+    KDA_KERNEL_QK_NORM_BWD = 10,
+    KDA_KERNEL_QK_NORM_DW = 11,
+    KDA_KERNEL_VERIFY = 12,
+    KDA_KERNEL_GDR_STEP = 13,
+    KDA_NUM_KERNELS = 14
 };
 int kda_profile_enable(int on);
 int kda_profile_read(double* total_ms, long long* launches);
