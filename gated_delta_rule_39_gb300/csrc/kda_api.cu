@@ -933,6 +933,9 @@ const char* kda_kernel_name(int kernel_id) {
         case KDA_KERNEL_QK_NORM_DW: return "qk_norm_dw_kernel";
         case KDA_KERNEL_VERIFY: return "verify_kernel";
         case KDA_KERNEL_GDR_STEP: return "gdr_step_kernel";
+        case KDA_KERNEL_GDR_MAP: return "gdr_map_kernel";
+        case KDA_KERNEL_GDR_PREP: return "gdr_prep_kernel";
+        case KDA_KERNEL_GDR_CHAIN: return "gdr_chain_kernel";
         default: return "unknown";
     }
 }

@@ -3,7 +3,7 @@
 #include <algorithm>
 #include <cmath>
 
-#include "kda_gdr.cuh"
+#include "kda_gdr_chunk.cuh"
 
 namespace kda {
 
@@ -14,7 +14,7 @@ size_t gdr_span(long long tokens, int heads, long long stride) {
 int gdr_validate(const GdrInputs& in, int B, int K, int V, const void* s0, int s0_dtype, const void* s1,
                  int s1_dtype, long long pool) {
     if (K != kDim || V != kDim) return KDA_ERR_UNSUPPORTED_DIM;
-    if (B < 0 || in.T < 0 || in.Hk < 1 || in.Hv < 1 || in.Hv % in.Hk) return KDA_ERR_SHAPE;
+    if (B < 0 || in.T < 0 || in.Hk < 1 || in.Hk > 65535 || in.Hv < 1 || in.Hv % in.Hk) return KDA_ERR_SHAPE;
     const long long tok = (long long)B * in.T;
     if (tok >= (1LL << 31) || tok * in.Hv * kDim >= (1LL << 40)) return KDA_ERR_SHAPE;
     if (pool < 0 || pool * in.Hv >= (1LL << 31) / 2) return KDA_ERR_SHAPE;
@@ -53,6 +53,14 @@ bool hits_inputs(const GdrInputs& in, long long tok, const void* p, size_t n) {
 
 bool states_clash(const void* s0, size_t n0, int d0, const void* s1, size_t n1, int d1) {
     return overlaps(s0, n0, s1, n1) && (s0 != s1 || d0 != d1);
+}
+
+// Where a call's chunks are; returns the bytes of the map of packed sequences (first chunk
+// of each, and whether the offsets are valid).
+size_t plan_chunks(bool varlen, int B, int T, int N, gdr::Chunks* c) {
+    c->per_seq = varlen ? 0 : (T + gdr::kC - 1) / gdr::kC;
+    c->total = varlen ? T / gdr::kC + N : B * c->per_seq;
+    return varlen ? align_up(((size_t)N + 2) * sizeof(int)) : 0;
 }
 
 }  // namespace
@@ -114,7 +122,7 @@ int kda_gdr_fwd(const void* q, const void* k, const void* v, const void* g, cons
                 long long q_stride, long long k_stride, long long v_stride, void* stream) {
     const bool varlen = cu_seqlens != nullptr;
     const int N = varlen ? num_seqs : B;
-    GdrStep P{};
+    GdrChunked P{};
     P.in = {static_cast<const __nv_bfloat16*>(q), static_cast<const __nv_bfloat16*>(k),
             static_cast<const __nv_bfloat16*>(v), q_stride, k_stride, v_stride, g, beta, gate_dtype,
             scale, cu_seqlens, nullptr, N, T, Hk, Hv};
@@ -133,37 +141,32 @@ int kda_gdr_fwd(const void* q, const void* k, const void* v, const void* g, cons
         overlaps(out, n_out, cu_seqlens, ((size_t)N + 1) * 4) ||
         overlaps(final_state, n_so, cu_seqlens, ((size_t)N + 1) * 4))
         return KDA_ERR_ALIAS;
-    int dev = 0;
-    int* err = nullptr;
-    rc = device_setup(&dev, &err);
+    int dev = 0, sms = 0;
+    rc = device_setup(&dev, &P.err, &sms);
     if (rc != KDA_OK) return rc;
-    cudaStream_t s = static_cast<cudaStream_t>(stream);
-    int* scratch = nullptr;
-    cudaError_t e = cudaSuccess;
-    if (varlen) {
-        e = cudaMallocAsync(reinterpret_cast<void**>(&scratch), align_up(((size_t)N + 2) * 4), s);
-        if (e != cudaSuccess) return cuda_fail(KDA_ERR_ALLOC, e);
-        Problem FP{};
-        FP.cu_seqlens = cu_seqlens;
-        FP.N = N;
-        FP.T = T;
-        FP.H = Hv;
-        SeqMap M{};
-        M.seq_order = scratch;
-        M.valid = scratch + N;
-        P.in.valid = M.valid;
-        e = timed_launch(KDA_KERNEL_SEQMAP, s, [&] { return launch_seqmap(FP, M, err, s); });
-    }
     P.out = static_cast<__nv_bfloat16*>(out);
-    P.state_in = initial_state;
-    P.in_dtype = initial_state_dtype;
-    P.state_out = final_state;
-    P.out_dtype = final_state_dtype;
-    P.pool = N;
-    P.err = err;
+    P.init_state = initial_state;
+    P.init_dtype = initial_state_dtype;
+    P.final_state = final_state;
+    P.final_dtype = final_state_dtype;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const size_t map_bytes = plan_chunks(varlen, B, T, N, &P.chunks);
+    unsigned char* scratch = nullptr;
+    cudaError_t e = cudaMallocAsync(reinterpret_cast<void**>(&scratch),
+                                    map_bytes + (size_t)P.chunks.total * Hv * gdr::kBlockBytes + kAlign, s);
+    if (e != cudaSuccess) return cuda_fail(KDA_ERR_ALLOC, e);
+    P.blocks = scratch + map_bytes;
+    if (varlen) {
+        int* first = reinterpret_cast<int*>(scratch);
+        P.chunks.first = first;
+        P.in.valid = first + N + 1;
+        e = timed_launch(KDA_KERNEL_GDR_MAP, s,
+                         [&] { return launch_gdr_map(P.in, first, first + N + 1, P.err, s); });
+    }
+    if (e == cudaSuccess) e = timed_launch(KDA_KERNEL_GDR_PREP, s, [&] { return launch_gdr_prep(P, s); });
     if (e == cudaSuccess)
-        e = timed_launch(KDA_KERNEL_GDR_STEP, s, [&] { return launch_gdr_step(P, s); });
-    if (scratch) cudaFreeAsync(scratch, s);
+        e = timed_launch(KDA_KERNEL_GDR_CHAIN, s, [&] { return launch_gdr_chain(P, sms, s); });
+    cudaFreeAsync(scratch, s);
     if (e != cudaSuccess) return cuda_fail(KDA_ERR_LAUNCH, e);
     return KDA_OK;
 }

@@ -1,0 +1,161 @@
+// The chunked form of the gated delta rule with one decay per value head: the layout of
+// its scratch and the tensor-core helpers its kernels share.
+//
+// A chunk is 64 tokens.  With G the running sum of g inside it, M_ij = e^(G_i - G_j) for
+// j <= i, A the strictly lower triangle of beta_i M_ij k_i.k_j, T = (I + A)^-1 and S the
+// state before it,
+//
+//   R = beta (V - e^G K S),  X = T R          (row j of X is the update d_j)
+//   O = scale (e^G Q S + (M . Q K^T) X)
+//   S <- e^(G_C) S + K^T (e^(G_C - G) X)
+//
+// T and P = M . Q K^T depend on queries, keys and gates alone: the prep kernel forms
+// them for all chunks in parallel; the chain kernel then walks the chunks of a sequence.
+//
+// Numerics: G, the decays and every product's accumulator are fp32, and so is the state
+// between chunks.  The operands of the tensor-core products are fp16: queries, keys (bf16
+// data, exact in fp16 for magnitudes of 2^-14 to 65,504), T, P, R, X and the rounded state.
+// fp16's 11 bits keep the result within 4e-4 of the exact one on unit keys, where bf16
+// operands gave 3e-3; its price is that keys, queries, values and states have to stay
+// below 65,504.  The inverse T is formed in fp32 with tf32 products between its blocks.
+#pragma once
+#include "kda_gdr.cuh"
+
+#ifndef KDA_SPIN_LIMIT
+#define KDA_SPIN_LIMIT (1LL << 32)   // cycles that a wait inside a kernel may take (about 2 s)
+#endif
+
+namespace kda {
+namespace gdr {
+
+constexpr int kC = 64;                        // tokens per chunk
+// One (chunk, value head)'s block of scratch: T and P as fp16 [64][64] tiles (128-byte rows
+// whose 16-byte units are stored at unit ^ (row & 7)), then fp32 b, b e^G, e^G, e^(G_C - G)
+// of its 64 tokens and e^(G_C).
+constexpr int kTileBytes = kC * kC * 2;
+constexpr int kGateFloats = 4 * kC + 4;
+constexpr int kBlockUsed = 2 * kTileBytes + kGateFloats * 4;   // 17,424
+constexpr int kBlockBytes = (kBlockUsed + 127) / 128 * 128;
+
+struct Chunks {           // where the chunks of each sequence are
+    const int* first;     // [N + 1] first chunk of each sequence (packed), or nullptr
+    int per_seq;          // fixed length: chunks of each sequence
+    int total;            // chunks in all (packed: an upper bound)
+};
+
+struct Span {
+    long long start;      // first token
+    int len;              // tokens
+    int chunk;            // first chunk
+};
+__device__ __forceinline__ Span span_of(const GdrInputs& I, const Chunks& C, int n) {
+    if (I.cu) return {I.cu[n], I.cu[n + 1] - I.cu[n], C.first[n]};
+    return {(long long)n * I.T, I.T, n * C.per_seq};
+}
+
+// ---- mbarriers ----------------------------------------------------------------------
+__device__ __forceinline__ void bar_init(uint64_t* b, int count) {
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;\n" ::"r"(smem_u32(b)), "r"(count));
+}
+__device__ __forceinline__ void bar_arrive(uint64_t* b) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(smem_u32(b)) : "memory");
+}
+// arrives once the thread's earlier cp.async copies have landed
+__device__ __forceinline__ void bar_arrive_copies(uint64_t* b) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];\n" ::"r"(smem_u32(b)) : "memory");
+}
+// Waits, as a whole warp, for a phase to end; after KDA_SPIN_LIMIT cycles records a timeout
+// and gives up (every lane gets the same answer).
+__device__ __forceinline__ bool bar_wait(uint64_t* b, unsigned parity, int* err) {
+    const long long t0 = clock64();
+    for (;;) {
+        unsigned ok;
+        asm volatile(
+            "{\n .reg .pred p;\n"
+            " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+            " selp.u32 %0, 1, 0, p;\n}\n"
+            : "=r"(ok) : "r"(smem_u32(b)), "r"(parity) : "memory");
+        if (__all_sync(0xFFFFFFFFu, ok)) return true;
+        if (__any_sync(0xFFFFFFFFu, clock64() - t0 > KDA_SPIN_LIMIT)) {
+            set_error(err, KDA_ERR_DEVICE_TIMEOUT);
+            return false;
+        }
+    }
+}
+
+// ---- fragments --------------------------------------------------------------------------
+__device__ __forceinline__ void ldsm(uint32_t (&r)[4], uint32_t a) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];\n"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
+}
+__device__ __forceinline__ void ldsm_t(uint32_t (&r)[4], uint32_t a) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];\n"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
+}
+__device__ __forceinline__ void stsm(uint32_t a, uint32_t r0, uint32_t r1, uint32_t r2, uint32_t r3) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1,%2,%3,%4};\n"
+                 ::"r"(a), "r"(r0), "r"(r1), "r"(r2), "r"(r3) : "memory");
+}
+__device__ __forceinline__ void stsm_t(uint32_t a, uint32_t r0, uint32_t r1, uint32_t r2, uint32_t r3) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};\n"
+                 ::"r"(a), "r"(r0), "r"(r1), "r"(r2), "r"(r3) : "memory");
+}
+// D += A(16x16 bf16, row) * B(16x8 bf16, col), fp32 accumulate
+__device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};\n"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ float bf16_lo(uint32_t u) { return __uint_as_float(u << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t u) { return __uint_as_float(u & 0xFFFF0000u); }
+// two bf16 values as two fp16 ones (exact between 2^-14 and 65,504)
+__device__ __forceinline__ uint32_t bf16_to_half2(uint32_t u) { return pack_half2(bf16_lo(u), bf16_hi(u)); }
+// fp32 bits rounded to tf32 (nearest, ties away): the tensor core reads the top 19 bits
+__device__ __forceinline__ uint32_t tf32_bits(float x) { return __float_as_uint(x) + 0x1000u; }
+
+// Shared-memory tiles of 16-bit elements whose rows hold a power of two of 16-byte units:
+// unit u of row r is at unit u ^ (r & 7), which spreads the 8 rows of an ldmatrix over the
+// banks.  kRow = bytes per row.
+template <int kRow>
+__device__ __forceinline__ uint32_t unit_at(uint32_t base, int row, int unit) {
+    return base + row * kRow + ((unit ^ (row & 7)) << 4);
+}
+// ldmatrix address of this lane for a 16 x 16 block as an A operand (or, stored transposed,
+// as two B operands): rows r0 .. r0 + 15, units u0, u0 + 1; the matrices come in the order
+// (rows 0-7, u0), (rows 8-15, u0), (rows 0-7, u0 + 1), (rows 8-15, u0 + 1)
+template <int kRow>
+__device__ __forceinline__ uint32_t a_addr(uint32_t base, int r0, int u0, int lane) {
+    return unit_at<kRow>(base, r0 + (lane & 15), u0 + (lane >> 4));
+}
+// the same for two B operands whose n runs along the rows and k along the units: matrices
+// (rows 0-7, u0), (rows 0-7, u0 + 1), (rows 8-15, u0), (rows 8-15, u0 + 1)
+template <int kRow>
+__device__ __forceinline__ uint32_t b_addr(uint32_t base, int r0, int u0, int lane) {
+    return unit_at<kRow>(base, r0 + (lane & 7) + ((lane >> 4) << 3), u0 + ((lane >> 3) & 1));
+}
+
+}  // namespace gdr
+
+struct GdrChunked {       // a chunked forward pass
+    GdrInputs in;
+    gdr::Chunks chunks;
+    unsigned char* blocks;            // [chunk][Hv] blocks of kBlockBytes
+    __nv_bfloat16* out;
+    const void* init_state;           // [N][Hv][128][128] or nullptr
+    int init_dtype;
+    void* final_state;                // or nullptr
+    int final_dtype;
+    int* err;
+};
+
+cudaError_t launch_gdr_map(const GdrInputs& in, int* first, int* valid, int* err, cudaStream_t s);
+cudaError_t launch_gdr_prep(const GdrChunked& P, cudaStream_t s);
+cudaError_t launch_gdr_chain(const GdrChunked& P, int sms, cudaStream_t s);
+
+}  // namespace kda

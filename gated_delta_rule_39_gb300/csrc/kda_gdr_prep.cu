@@ -1,0 +1,315 @@
+// Chunk-parallel part of the gated delta rule with one decay per value head: where the
+// chunks of packed sequences are (map), and each chunk's T = (I + A)^-1, P = M . Q K^T and
+// decays (prep).
+#include "kda_gdr_chunk.cuh"
+
+namespace kda {
+namespace {
+
+using namespace gdr;
+
+// ---- map: checks cu_seqlens, first[n] = chunks of the sequences before n ------------------
+constexpr int kMapThreads = 1024;
+
+__global__ void __launch_bounds__(kMapThreads) gdr_map_kernel(GdrInputs I, int* first, int* valid, int* err) {
+    __shared__ int sums[kMapThreads / 32];
+    __shared__ int bad;
+    const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+    if (tid == 0) bad = I.cu[0] != 0 || I.cu[I.N] != I.T;
+    __syncthreads();
+    for (int n = tid; n < I.N; n += kMapThreads)
+        if (I.cu[n + 1] < I.cu[n]) bad = 1;
+    __syncthreads();
+    if (tid == 0) {
+        *valid = !bad;
+        if (bad) set_error(err, KDA_ERR_BAD_SEQLENS);
+    }
+    if (bad) return;
+    int before = 0;
+    for (int base = 0; base < I.N; base += kMapThreads) {
+        const int n = base + tid;
+        const int c = n < I.N ? (I.cu[n + 1] - I.cu[n] + kC - 1) / kC : 0;
+        int x = c;                     // inclusive sums of the warp, then of the warps before
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xFFFFFFFFu, x, o);
+            if (lane >= o) x += y;
+        }
+        __syncthreads();               // the last round's sums have been read
+        if (lane == 31) sums[w] = x;
+        __syncthreads();
+        int all = 0;
+        for (int i = 0; i < kMapThreads / 32; ++i) {
+            if (i == w) x += all;
+            all += sums[i];
+        }
+        if (n < I.N) first[n] = before + x - c;
+        before += all;
+    }
+    if (tid == 0) first[I.N] = before;
+}
+
+// ---- prep -------------------------------------------------------------------------------
+// One CTA of 4 warps per (chunk, query/key head).  Warp w forms rows 16 w .. 16 w + 15 of
+// K K^T and Q K^T on tensor cores (bf16 data, fp32 sums; kept in registers for all value
+// heads of the group), and per value head: the gates' running sum, A and P, and
+// T = (I + A)^-1: the four 16 x 16 diagonal blocks by forward substitution in fp32 (a lane
+// owns a column), then T21 = -T22 A21 T11 for blocks of 16 and of 32 with tf32 products.
+constexpr int kPrepThreads = 128;
+constexpr int kLd = 68;               // row length of the fp32 tiles: rows 4 banks apart
+
+struct PrepSmem {
+    __align__(128) unsigned char k[kC * kDim * 2];
+    __align__(128) unsigned char q[kC * kDim * 2];     // later: P as fp16
+    __align__(16) float a[kC][kLd];                    // A (strictly lower)
+    __align__(16) float t[kC][kLd];                    // T (lower blocks)
+    float g[kC];                                       // running sum of g in base 2
+    float b[kC];
+};
+
+// rows [0, 64) of one head, zeros from row `rows` on, into a tile of 256-byte rows
+__device__ __forceinline__ void load_tile(uint32_t dst, const __nv_bfloat16* src, long long stride, int rows,
+                                          int tid) {
+#pragma unroll
+    for (int i = 0; i < kC * 16 / kPrepThreads; ++i) {
+        const int unit = tid & 15, row = (tid >> 4) + i * (kPrepThreads / 16);
+        const int bytes = row < rows ? 16 : 0;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n"
+                     ::"r"(unit_at<256>(dst, row, unit)), "l"(src + (row < rows ? row * stride : 0) + unit * 8),
+                       "r"(bytes) : "memory");
+    }
+}
+
+// C(16 x 8 kN) = A(rows ar .., cols ac ..) B(rows br .., cols bc ..), 8 kK deep, from fp32 tiles
+template <int kN, int kK>
+__device__ __forceinline__ void tf32_product(float (&c)[kN][4], const float (*A)[kLd], int ar, int ac,
+                                             const float (*B)[kLd], int br, int bc, int lane) {
+    const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+    for (int n = 0; n < kN; ++n) c[n][0] = c[n][1] = c[n][2] = c[n][3] = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kK; ++k) {
+        const uint32_t a[4] = {tf32_bits(A[ar + g][ac + 8 * k + t]), tf32_bits(A[ar + g + 8][ac + 8 * k + t]),
+                               tf32_bits(A[ar + g][ac + 8 * k + t + 4]),
+                               tf32_bits(A[ar + g + 8][ac + 8 * k + t + 4])};
+#pragma unroll
+        for (int n = 0; n < kN; ++n)
+            mma_tf32(c[n], a, tf32_bits(B[br + 8 * k + t][bc + 8 * n + g]),
+                     tf32_bits(B[br + 8 * k + t + 4][bc + 8 * n + g]));
+    }
+}
+// out(16 x 8 kN at ar.., bc..) = -F B: F (16 x 8 kK) from accumulators.  An accumulator holds
+// columns 2 t and 2 t + 1 where an A operand wants t and t + 4: the depth is walked in
+// that order on both sides.
+template <int kN, int kK>
+__device__ __forceinline__ void tf32_second(float (*T)[kLd], int orow, int ocol, const float (&f)[kK][4],
+                                            int br, int lane) {
+    const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+    for (int n = 0; n < kN; ++n) {
+        float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int k = 0; k < kK; ++k) {
+            const uint32_t a[4] = {tf32_bits(f[k][0]), tf32_bits(f[k][2]), tf32_bits(f[k][1]), tf32_bits(f[k][3])};
+            mma_tf32(c, a, tf32_bits(T[br + 8 * k + 2 * t][ocol + 8 * n + g]),
+                     tf32_bits(T[br + 8 * k + 2 * t + 1][ocol + 8 * n + g]));
+        }
+        T[orow + g][ocol + 8 * n + 2 * t] = -c[0];
+        T[orow + g][ocol + 8 * n + 2 * t + 1] = -c[1];
+        T[orow + g + 8][ocol + 8 * n + 2 * t] = -c[2];
+        T[orow + g + 8][ocol + 8 * n + 2 * t + 1] = -c[3];
+    }
+}
+
+__global__ void __launch_bounds__(kPrepThreads) gdr_prep_kernel(GdrChunked P) {
+    extern __shared__ __align__(128) unsigned char raw[];
+    PrepSmem& S = *reinterpret_cast<PrepSmem*>(raw);
+    const GdrInputs& I = P.in;
+    const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, g = lane >> 2, t = lane & 3;
+    const int chunk = blockIdx.x, hk = blockIdx.y;
+    int n, c;
+    if (I.cu) {
+        if (!*I.valid || chunk >= P.chunks.first[I.N]) return;
+        int lo = 0, hi = I.N;          // the last sequence whose first chunk is at most `chunk`
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) / 2;
+            if (P.chunks.first[mid] <= chunk) lo = mid;
+            else hi = mid;
+        }
+        n = lo;
+        c = chunk - P.chunks.first[n];
+    } else {
+        n = chunk / P.chunks.per_seq;
+        c = chunk % P.chunks.per_seq;
+    }
+    const Span span = span_of(I, P.chunks, n);
+    const long long tok = span.start + (long long)c * kC;
+    const int rows = min(kC, span.len - c * kC);
+    const uint32_t sk = smem_u32(S.k), sq = smem_u32(S.q);
+    load_tile(sk, I.k + tok * I.k_stride + hk * kDim, I.k_stride, rows, tid);
+    load_tile(sq, I.q + tok * I.q_stride + hk * kDim, I.q_stride, rows, tid);
+    cp_async_commit();
+    cp_async_wait<0>();
+    __syncthreads();
+    // rows 16 w ..  of K K^T and Q K^T, columns 0 .. 16 w + 15
+    float kk[8][4], qk[8][4];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) kk[i][j] = qk[i][j] = 0.0f;
+#pragma unroll
+    for (int ks = 0; ks < 8; ++ks) {
+        uint32_t ak[4], aq[4];
+        ldsm(ak, a_addr<256>(sk, 16 * w, 2 * ks, lane));
+        ldsm(aq, a_addr<256>(sq, 16 * w, 2 * ks, lane));
+#pragma unroll
+        for (int np = 0; np < 4; ++np) {
+            if (np > w) break;
+            uint32_t b[4];
+            ldsm(b, b_addr<256>(sk, 16 * np, 2 * ks, lane));
+            mma_bf16(kk[2 * np], ak, b[0], b[1]);
+            mma_bf16(kk[2 * np + 1], ak, b[2], b[3]);
+            mma_bf16(qk[2 * np], aq, b[0], b[1]);
+            mma_bf16(qk[2 * np + 1], aq, b[2], b[3]);
+        }
+    }
+    const int share = I.Hv / I.Hk;
+    for (int h = hk * share; h < (hk + 1) * share; ++h) {
+        __syncthreads();               // Q, and the last head's tiles, have been read
+        unsigned char* block = P.blocks + ((size_t)chunk * I.Hv + h) * kBlockBytes;
+        if (w == 0) {                  // two tokens per lane
+            const size_t at = (size_t)(tok + 2 * lane) * I.Hv + h;
+            float g0 = 0.0f, g1 = 0.0f, b0 = 0.0f, b1 = 0.0f;
+            if (2 * lane < rows) {
+                g0 = load_gate(I.g, I.gate_dtype, at) * kLog2e;
+                b0 = load_gate(I.beta, I.gate_dtype, at);
+            }
+            if (2 * lane + 1 < rows) {
+                g1 = load_gate(I.g, I.gate_dtype, at + I.Hv) * kLog2e;
+                b1 = load_gate(I.beta, I.gate_dtype, at + I.Hv);
+            }
+            // 2^-160 is 0 in fp32 already: lower logs (-inf) only would spoil the differences
+            g0 = g0 < -160.0f ? -160.0f : g0;
+            g1 = g1 < -160.0f ? -160.0f : g1;
+            float x = g0 + g1;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const float y = __shfl_up_sync(0xFFFFFFFFu, x, o);
+                if (lane >= o) x += y;
+            }
+            const float last = __shfl_sync(0xFFFFFFFFu, x, 31);
+            const float x0 = x - g1;
+            S.g[2 * lane] = x0;
+            S.g[2 * lane + 1] = x;
+            S.b[2 * lane] = b0;
+            S.b[2 * lane + 1] = b1;
+            float* gates = reinterpret_cast<float*>(block + 2 * kTileBytes);
+            const float e0 = ex2_approx(x0), e1 = ex2_approx(x);
+            reinterpret_cast<float2*>(gates)[lane] = make_float2(b0, b1);
+            reinterpret_cast<float2*>(gates + kC)[lane] = make_float2(b0 * e0, b1 * e1);
+            reinterpret_cast<float2*>(gates + 2 * kC)[lane] = make_float2(e0, e1);
+            reinterpret_cast<float2*>(gates + 3 * kC)[lane] = make_float2(ex2_approx(last - x0), ex2_approx(last - x));
+            if (lane == 0) gates[4 * kC] = ex2_approx(last);
+        }
+        __syncthreads();
+        // A in fp32 and P in fp16
+        const float gi0 = S.g[16 * w + g], gi1 = S.g[16 * w + g + 8];
+        const float bi0 = S.b[16 * w + g], bi1 = S.b[16 * w + g + 8];
+#pragma unroll
+        for (int np = 0; np < 4; ++np) {
+            uint32_t p[4] = {0u, 0u, 0u, 0u};
+            if (np <= w) {
+                float pv[2][4];
+#pragma unroll
+                for (int m = 0; m < 2; ++m) {
+                    const int nt = 2 * np + m, j = 8 * nt + 2 * t, i0 = 16 * w + g, i1 = i0 + 8;
+                    const float gj0 = S.g[j], gj1 = S.g[j + 1];
+                    const float m00 = j <= i0 ? ex2_approx(gi0 - gj0) : 0.0f;
+                    const float m01 = j + 1 <= i0 ? ex2_approx(gi0 - gj1) : 0.0f;
+                    const float m10 = j <= i1 ? ex2_approx(gi1 - gj0) : 0.0f;
+                    const float m11 = j + 1 <= i1 ? ex2_approx(gi1 - gj1) : 0.0f;
+                    *reinterpret_cast<float2*>(&S.a[i0][j]) =
+                        make_float2(j < i0 ? bi0 * m00 * kk[nt][0] : 0.0f, j + 1 < i0 ? bi0 * m01 * kk[nt][1] : 0.0f);
+                    *reinterpret_cast<float2*>(&S.a[i1][j]) =
+                        make_float2(j < i1 ? bi1 * m10 * kk[nt][2] : 0.0f, j + 1 < i1 ? bi1 * m11 * kk[nt][3] : 0.0f);
+                    pv[m][0] = j <= i0 ? m00 * qk[nt][0] : 0.0f;
+                    pv[m][1] = j + 1 <= i0 ? m01 * qk[nt][1] : 0.0f;
+                    pv[m][2] = j <= i1 ? m10 * qk[nt][2] : 0.0f;
+                    pv[m][3] = j + 1 <= i1 ? m11 * qk[nt][3] : 0.0f;
+                }
+                p[0] = pack_half2(pv[0][0], pv[0][1]);
+                p[1] = pack_half2(pv[0][2], pv[0][3]);
+                p[2] = pack_half2(pv[1][0], pv[1][1]);
+                p[3] = pack_half2(pv[1][2], pv[1][3]);
+            }
+            stsm(a_addr<128>(sq, 16 * w, 2 * np, lane), p[0], p[1], p[2], p[3]);
+        }
+        __syncwarp();
+        // inverse of this warp's diagonal block, a column per lane
+        if (lane < 16) {
+            float x[16];
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                float s = r == lane ? 1.0f : 0.0f;
+#pragma unroll
+                for (int m = 0; m < r; ++m) s = fmaf(-S.a[16 * w + r][16 * w + m], x[m], s);
+                x[r] = s;
+                S.t[16 * w + r][16 * w + lane] = s;
+            }
+        }
+        __syncthreads();
+        {   // blocks of 16: T21 = -(T22 A21) T11, half of the columns per warp
+            const int r0 = 32 * (w >> 1);
+            float f[2][4];
+            tf32_product<2, 2>(f, S.t, r0 + 16, r0 + 16, S.a, r0 + 16, r0, lane);
+            tf32_second<1, 2>(S.t, r0 + 16, r0 + 8 * (w & 1), f, r0, lane);
+            // zeros above the diagonal blocks, which the next products read
+            if (w & 1) {
+#pragma unroll
+                for (int i = lane; i < 16 * 16; i += 32) S.t[r0 + (i >> 4)][r0 + 16 + (i & 15)] = 0.0f;
+            }
+        }
+        __syncthreads();
+        {   // blocks of 32: 16 rows and 16 columns per warp
+            const int r0 = 32 + 16 * (w >> 1);
+            float f[4][4];
+            tf32_product<4, 4>(f, S.t, r0, 32, S.a, 32, 0, lane);
+            tf32_second<2, 4>(S.t, r0, 16 * (w & 1), f, 0, lane);
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kC * 8 / kPrepThreads; ++i) {
+            const int unit = tid & 7, row = (tid >> 3) + i * (kPrepThreads / 8);
+            uint4 x = make_uint4(0u, 0u, 0u, 0u);
+            if (8 * unit <= row) {
+                const float4 lo = *reinterpret_cast<const float4*>(&S.t[row][8 * unit]);
+                const float4 hi = *reinterpret_cast<const float4*>(&S.t[row][8 * unit + 4]);
+                const int d = row - 8 * unit;      // columns after the diagonal are not part of T
+                x.x = pack_half2(lo.x, d >= 1 ? lo.y : 0.0f);
+                x.y = pack_half2(d >= 2 ? lo.z : 0.0f, d >= 3 ? lo.w : 0.0f);
+                x.z = pack_half2(d >= 4 ? hi.x : 0.0f, d >= 5 ? hi.y : 0.0f);
+                x.w = pack_half2(d >= 6 ? hi.z : 0.0f, d >= 7 ? hi.w : 0.0f);
+            }
+            const int at = row * 128 + ((unit ^ (row & 7)) << 4);
+            *reinterpret_cast<uint4*>(block + at) = x;
+            *reinterpret_cast<uint4*>(block + kTileBytes + at) = *reinterpret_cast<const uint4*>(S.q + at);
+        }
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_gdr_map(const GdrInputs& in, int* first, int* valid, int* err, cudaStream_t s) {
+    gdr_map_kernel<<<1, kMapThreads, 0, s>>>(in, first, valid, err);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_gdr_prep(const GdrChunked& P, cudaStream_t s) {
+    if (P.chunks.total == 0) return cudaSuccess;
+    const cudaError_t e = allow_smem<gdr_prep_kernel>(sizeof(PrepSmem));
+    if (e != cudaSuccess) return e;
+    gdr_prep_kernel<<<dim3(P.chunks.total, P.in.Hk), kPrepThreads, sizeof(PrepSmem), s>>>(P);
+    return cudaGetLastError();
+}
+
+}  // namespace kda

@@ -491,7 +491,10 @@ enum {
     KDA_KERNEL_QK_NORM_DW = 11,
     KDA_KERNEL_VERIFY = 12,
     KDA_KERNEL_GDR_STEP = 13,
-    KDA_NUM_KERNELS = 14
+    KDA_KERNEL_GDR_MAP = 14,
+    KDA_KERNEL_GDR_PREP = 15,
+    KDA_KERNEL_GDR_CHAIN = 16,
+    KDA_NUM_KERNELS = 17
 };
 int kda_profile_enable(int on);
 int kda_profile_read(double* total_ms, long long* launches);
