@@ -14,13 +14,13 @@ import ctypes
 import os
 
 from . import _operators
-from ._operators import (kda_gdr_fwd, kda_gdr_step, kda_qk_norm, kda_qk_norm_bwd,
-                         kda_verify_drafts)
+from ._operators import (kda_gdr_bwd, kda_gdr_bwd_workspace_bytes, kda_gdr_fwd, kda_gdr_step,
+                         kda_qk_norm, kda_qk_norm_bwd, kda_verify_drafts)
 
 __all__ = ["KdaError", "kda_fwd", "kda_fwd_segments", "kda_fwd_host", "kda_fwd_noalloc",
            "kda_decode", "kda_bwd", "kda_bwd_workspace_bytes",
            "kda_qk_norm", "kda_qk_norm_bwd", "kda_gdr_fwd", "kda_gdr_step",
-           "kda_verify_drafts",
+           "kda_gdr_bwd", "kda_gdr_bwd_workspace_bytes", "kda_verify_drafts",
            "kda_fwd_get_error", "kda_status_string",
            "kda_last_cuda_error",
            "kda_fwd_workspace_bytes", "kda_profile_enable", "kda_profile_read",
@@ -32,12 +32,13 @@ _LIB_PATH = os.path.join(_HERE, "_lib", "libkda.so")
 
 KDA_BF16 = 0
 KDA_F32 = 1
-KDA_NUM_KERNELS = 17
+KDA_NUM_KERNELS = 20
 KERNEL_NAMES = ("seqmap_kernel", "fused_kernel", "decode_kernel", "combine_kernel",
                 "segprep_kernel", "segfinal_kernel", "bwd_kernel", "bwd_finish_kernel",
                 "bwd_reduce_kernel", "qk_norm_kernel", "qk_norm_bwd_kernel",
                 "qk_norm_dw_kernel", "verify_kernel", "gdr_step_kernel",
-                "gdr_map_kernel", "gdr_prep_kernel", "gdr_chain_kernel")
+                "gdr_map_kernel", "gdr_prep_kernel", "gdr_chain_kernel", "gdr_amax_kernel",
+                "gdr_bwd_chain_kernel", "gdr_bwd_chunk_kernel")
 
 _lib = None
 _vp = ctypes.c_void_p

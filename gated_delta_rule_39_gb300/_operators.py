@@ -19,10 +19,13 @@ def declare(lib):
             ("kda_qk_norm", [_vp] * 4 + norm + turn),
             ("kda_qk_norm_bwd", [_vp] * 6 + norm + [_vp, _vp] + turn),
             ("kda_gdr_fwd", rule + [_vp, _vp, _i, _vp, _i, _vp, _i] + sizes),
+            ("kda_gdr_bwd", rule + [_vp, _i, _vp, _vp, _i] + [_vp] * 6 + [_i, _vp, _i] + sizes),
             ("kda_gdr_step", rule + [_vp, _vp, _i, _vp, _i, _vp, _i, _vp] + sizes),
             ("kda_verify_drafts", [_vp, _vp, _i] + [_vp] * 6 + [_i] * 3 + [_vp])):
         fn = getattr(lib, name)
         fn.argtypes, fn.restype = args, _i
+    lib.kda_gdr_bwd_workspace_bytes.argtypes = [_i] * 6
+    lib.kda_gdr_bwd_workspace_bytes.restype = ctypes.c_size_t
     return lib
 
 
@@ -223,6 +226,41 @@ def kda_gdr_fwd(q, k, v, g, beta, scale: float, out, initial_state=None, final_s
     states = _states(dev, (N, Hv, K, V), initial_state=initial_state, final_state=final_state)
     _call("kda_gdr_fwd", dev, stream, *head, scale, _ptr(out), *states, _ptr(cu_seqlens), num, B, T,
           Hk, Hv, K, V, *strides)
+
+
+def kda_gdr_bwd(q, k, v, g, beta, scale: float, d_out, initial_state=None, d_final_state=None,
+                cu_seqlens=None, stream=None, d_initial_state: bool = True) -> dict:
+    """Gradients of a loss with respect to ``kda_gdr_fwd``'s inputs, on CUDA tensors
+    (asynchronous on ``stream``).
+
+    d_out: bf16 [B, T, Hv, 128] = dL/d(out); d_final_state: optional bf16 or fp32
+    [N, Hv, 128, 128] = dL/d(final state).  Other arguments as ``kda_gdr_fwd``.  Returns dq, dk
+    (bf16 [B, T, Hk, 128]), dv (bf16 [B, T, Hv, 128]), dg, dbeta ([B, T, Hv] of the gates' type)
+    and, with an initial state (unless d_initial_state is False), d_initial_state of its type.
+    """
+    import torch
+    dev, head, (B, T, Hk, Hv, K, V), strides = _rule_args("kda_gdr_bwd", q, k, v, g, beta)
+    _dense(d_out, "d_out", (torch.bfloat16,), (B, T, Hv, V), dev)
+    N, num = _sequences(cu_seqlens, B, dev)
+    states = _states(dev, (N, Hv, K, V), initial_state=initial_state, d_final_state=d_final_state)
+    r = {"dq": torch.empty((B, T, Hk, K), dtype=q.dtype, device=dev),
+         "dk": torch.empty((B, T, Hk, K), dtype=q.dtype, device=dev),
+         "dv": torch.empty((B, T, Hv, V), dtype=q.dtype, device=dev),
+         "dg": torch.empty_like(g), "dbeta": torch.empty_like(beta)}
+    ds = None
+    if d_initial_state and initial_state is not None:
+        ds = r["d_initial_state"] = torch.empty_like(initial_state)
+    _call("kda_gdr_bwd", dev, stream, *head, scale, *states[:2], _ptr(d_out), *states[2:],
+          _ptr(r["dq"]), _ptr(r["dk"]), _ptr(r["dv"]), _ptr(r["dg"]), _ptr(r["dbeta"]), _ptr(ds),
+          int(ds is not None and ds.dtype == torch.float32), _ptr(cu_seqlens), num, B, T, Hk, Hv, K, V,
+          *strides)
+    return r
+
+
+def kda_gdr_bwd_workspace_bytes(B: int, T: int, Hk: int, Hv: int, num_seqs: int = 0,
+                                varlen: bool = False) -> int:
+    import gated_delta_rule_39_gb300 as kda
+    return int(kda.load_library().kda_gdr_bwd_workspace_bytes(B, T, Hk, Hv, num_seqs, int(varlen)))
 
 
 def kda_gdr_step(q, k, v, g, beta, scale: float, out=None, state_in=None, state_out=None,

@@ -63,6 +63,25 @@ size_t plan_chunks(bool varlen, int B, int T, int N, gdr::Chunks* c) {
     return varlen ? align_up(((size_t)N + 2) * sizeof(int)) : 0;
 }
 
+// Scratch of a backward pass (bytes from its start): the map of packed sequences, the
+// largest gradients, and per (chunk, value head) a block, S^T, X^T, dS^T and Y^T.
+struct BwdLayout {
+    gdr::Chunks chunks{};
+    size_t amax, blocks, states, xs, dstates, ys, total;
+};
+BwdLayout bwd_layout(bool varlen, int B, int T, int Hk, int Hv, int N) {
+    BwdLayout L{};
+    L.amax = plan_chunks(varlen, B, T, N, &L.chunks);
+    const size_t units = (size_t)L.chunks.total * Hv;
+    L.blocks = L.amax + align_up((size_t)N * Hk * 4);
+    L.states = L.blocks + units * gdr::kBlockBytes;
+    L.xs = align_up(L.states + units * gdr::kStateTile);
+    L.dstates = L.xs + units * gdr::kTokenTile;
+    L.ys = L.dstates + units * gdr::kStateTile;
+    L.total = L.ys + units * gdr::kTokenTile + kAlign;
+    return L;
+}
+
 }  // namespace
 }  // namespace kda
 
@@ -166,6 +185,100 @@ int kda_gdr_fwd(const void* q, const void* k, const void* v, const void* g, cons
     if (e == cudaSuccess) e = timed_launch(KDA_KERNEL_GDR_PREP, s, [&] { return launch_gdr_prep(P, s); });
     if (e == cudaSuccess)
         e = timed_launch(KDA_KERNEL_GDR_CHAIN, s, [&] { return launch_gdr_chain(P, sms, s); });
+    cudaFreeAsync(scratch, s);
+    if (e != cudaSuccess) return cuda_fail(KDA_ERR_LAUNCH, e);
+    return KDA_OK;
+}
+
+size_t kda_gdr_bwd_workspace_bytes(int B, int T, int Hk, int Hv, int num_seqs, int varlen) {
+    if (B < 1 || T < 0 || Hk < 1 || Hv < 1 || (varlen && num_seqs < 1)) return 0;
+    return bwd_layout(varlen != 0, B, T, Hk, Hv, varlen ? num_seqs : B).total;
+}
+
+int kda_gdr_bwd(const void* q, const void* k, const void* v, const void* g, const void* beta,
+                int gate_dtype, float scale, const void* initial_state, int initial_state_dtype,
+                const void* d_out, const void* d_final_state, int d_final_state_dtype, void* dq, void* dk,
+                void* dv, void* dg, void* dbeta, void* d_initial_state, int d_initial_state_dtype,
+                const int32_t* cu_seqlens, int num_seqs, int B, int T, int Hk, int Hv, int K, int V,
+                long long q_stride, long long k_stride, long long v_stride, void* stream) {
+    const bool varlen = cu_seqlens != nullptr;
+    const int N = varlen ? num_seqs : B;
+    GdrBackward P{};
+    GdrInputs& in = P.fwd.in;
+    in = {static_cast<const __nv_bfloat16*>(q), static_cast<const __nv_bfloat16*>(k),
+          static_cast<const __nv_bfloat16*>(v), q_stride, k_stride, v_stride, g, beta, gate_dtype,
+          scale, cu_seqlens, nullptr, N, T, Hk, Hv};
+    if (B < 1 || (varlen && (B != 1 || num_seqs < 1))) return KDA_ERR_SHAPE;
+    int rc = gdr_validate(in, B, K, V, initial_state, initial_state_dtype, d_final_state,
+                          d_final_state_dtype, N);
+    if (rc != KDA_OK) return rc;
+    if (d_initial_state && d_initial_state_dtype != KDA_BF16 && d_initial_state_dtype != KDA_F32)
+        return KDA_ERR_DTYPE;
+    const long long tok = (long long)B * T;
+    if (tok > 0 && (!d_out || !dq || !dk || !dv || !dg || !dbeta)) return KDA_ERR_NULL;
+    for (const void* p : {d_out, static_cast<const void*>(dq), static_cast<const void*>(dk),
+                          static_cast<const void*>(dv), static_cast<const void*>(d_initial_state)})
+        if (!aligned16(p)) return KDA_ERR_ALIGN;
+    const size_t gate = gate_dtype == KDA_F32 ? 4 : 2;
+    if (reinterpret_cast<uintptr_t>(dg) % gate || reinterpret_cast<uintptr_t>(dbeta) % gate ||
+        reinterpret_cast<uintptr_t>(cu_seqlens) % 4)
+        return KDA_ERR_ALIGN;
+    const size_t nk = (size_t)tok * Hk * kDim * 2, nv = (size_t)tok * Hv * kDim * 2, ng = (size_t)tok * Hv * gate;
+    const void* out_p[] = {dq, dk, dv, dg, dbeta, d_initial_state};
+    const size_t out_n[] = {nk, nk, nv, ng, ng, state_bytes(N, Hv, d_initial_state_dtype)};
+    const void* in_p[] = {initial_state, d_out, d_final_state, cu_seqlens};
+    const size_t in_n[] = {state_bytes(N, Hv, initial_state_dtype), nv, state_bytes(N, Hv, d_final_state_dtype),
+                           ((size_t)N + 1) * 4};
+    for (int o = 0; o < 6; ++o) {
+        if (hits_inputs(in, tok, out_p[o], out_n[o])) return KDA_ERR_ALIAS;
+        for (int i = 0; i < 4; ++i)
+            if (overlaps(out_p[o], out_n[o], in_p[i], in_n[i])) return KDA_ERR_ALIAS;
+        for (int o2 = o + 1; o2 < 6; ++o2)
+            if (overlaps(out_p[o], out_n[o], out_p[o2], out_n[o2])) return KDA_ERR_ALIAS;
+    }
+    int dev = 0, sms = 0;
+    rc = device_setup(&dev, &P.fwd.err, &sms);
+    if (rc != KDA_OK) return rc;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const BwdLayout L = bwd_layout(varlen, B, T, Hk, Hv, N);
+    unsigned char* scratch = nullptr;
+    cudaError_t e = cudaMallocAsync(reinterpret_cast<void**>(&scratch), L.total, s);
+    if (e != cudaSuccess) return cuda_fail(KDA_ERR_ALLOC, e);
+    P.fwd.chunks = L.chunks;
+    P.fwd.blocks = scratch + L.blocks;
+    P.fwd.init_state = initial_state;
+    P.fwd.init_dtype = initial_state_dtype;
+    P.fwd.states = scratch + L.states;
+    P.fwd.xs = scratch + L.xs;
+    P.dout = static_cast<const __nv_bfloat16*>(d_out);
+    P.dfinal = d_final_state;
+    P.dfinal_dtype = d_final_state_dtype;
+    P.amax = reinterpret_cast<unsigned*>(scratch + L.amax);
+    P.dstates = scratch + L.dstates;
+    P.ys = scratch + L.ys;
+    P.dq = static_cast<__nv_bfloat16*>(dq);
+    P.dk = static_cast<__nv_bfloat16*>(dk);
+    P.dv = static_cast<__nv_bfloat16*>(dv);
+    P.dg = dg;
+    P.dbeta = dbeta;
+    P.dinit = d_initial_state;
+    P.dinit_dtype = d_initial_state_dtype;
+    if (varlen) {
+        int* first = reinterpret_cast<int*>(scratch);
+        P.fwd.chunks.first = first;
+        in.valid = first + N + 1;
+        e = timed_launch(KDA_KERNEL_GDR_MAP, s,
+                         [&] { return launch_gdr_map(in, first, first + N + 1, P.fwd.err, s); });
+    }
+    if (e == cudaSuccess) e = cudaMemsetAsync(P.amax, 0, (size_t)N * Hk * 4, s);
+    if (e == cudaSuccess) e = timed_launch(KDA_KERNEL_GDR_AMAX, s, [&] { return launch_gdr_amax(P, s); });
+    if (e == cudaSuccess) e = timed_launch(KDA_KERNEL_GDR_PREP, s, [&] { return launch_gdr_prep(P.fwd, s); });
+    if (e == cudaSuccess)
+        e = timed_launch(KDA_KERNEL_GDR_CHAIN, s, [&] { return launch_gdr_chain(P.fwd, sms, s); });
+    if (e == cudaSuccess)
+        e = timed_launch(KDA_KERNEL_GDR_BWD_CHAIN, s, [&] { return launch_gdr_bwd_chain(P, sms, s); });
+    if (e == cudaSuccess)
+        e = timed_launch(KDA_KERNEL_GDR_BWD_CHUNK, s, [&] { return launch_gdr_bwd_chunk(P, s); });
     cudaFreeAsync(scratch, s);
     if (e != cudaSuccess) return cuda_fail(KDA_ERR_LAUNCH, e);
     return KDA_OK;

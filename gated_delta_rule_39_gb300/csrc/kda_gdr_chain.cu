@@ -62,7 +62,7 @@ __device__ __forceinline__ void store_state(void* p, int dtype, size_t i, float 
 }
 
 // ---- producers ----------------------------------------------------------------------------
-template <int NW>
+template <int NW, bool kSave>
 __device__ void produce(const GdrChunked& P, ChainSmem<NW>& S, const Span& span, int nch, int h, int part,
                         int p) {
     const GdrInputs& I = P.in;
@@ -80,7 +80,7 @@ __device__ void produce(const GdrChunked& P, ChainSmem<NW>& S, const Span& span,
             kr[i] = qr[i] = make_uint4(0u, 0u, 0u, 0u);
             if (row + row0 < span.len) {
                 kr[i] = __ldg(reinterpret_cast<const uint4*>(kp + row * I.k_stride));
-                qr[i] = __ldg(reinterpret_cast<const uint4*>(qp + row * I.q_stride));
+                if (!kSave) qr[i] = __ldg(reinterpret_cast<const uint4*>(qp + row * I.q_stride));
             }
         }
     };
@@ -105,7 +105,7 @@ __device__ void produce(const GdrChunked& P, ChainSmem<NW>& S, const Span& span,
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             *reinterpret_cast<uint4*>(G.k + dst + 2048 * i) = half4(kr[i]);
-            *reinterpret_cast<uint4*>(G.q + dst + 2048 * i) = half4(qr[i]);
+            if (!kSave) *reinterpret_cast<uint4*>(G.q + dst + 2048 * i) = half4(qr[i]);
         }
         bar_arrive(&S.full[st]);
         return true;
@@ -179,8 +179,8 @@ __device__ void chain(const GdrChunked& P, ChainSmem<NW>& S, int nch, int w, int
 #pragma unroll
             for (int m = 0; m < 2; ++m) {
                 const int nt = 2 * np + m;
-                const float2 b = *reinterpret_cast<const float2*>(gate + 8 * nt + 2 * t);
-                const float2 be = *reinterpret_cast<const float2*>(gate + kC + 8 * nt + 2 * t);
+                const float2 b = *reinterpret_cast<const float2*>(gate + kGateB + 8 * nt + 2 * t);
+                const float2 be = *reinterpret_cast<const float2*>(gate + kGateBe + 8 * nt + 2 * t);
                 rf[np][2 * m] = pack_half2(b.x * bf16_lo(vr[2 * m]) - be.x * y[nt][0],
                                            b.y * bf16_hi(vr[2 * m]) - be.y * y[nt][1]);
                 rf[np][2 * m + 1] = pack_half2(b.x * bf16_lo(vr[2 * m + 1]) - be.x * y[nt][2],
@@ -216,11 +216,11 @@ __device__ void chain(const GdrChunked& P, ChainSmem<NW>& S, int nch, int w, int
         for (int ks = 0; ks < 4; ++ks)
 #pragma unroll
             for (int m = 0; m < 2; ++m) {
-                const float2 ed = *reinterpret_cast<const float2*>(gate + 3 * kC + 16 * ks + 8 * m + 2 * t);
+                const float2 ed = *reinterpret_cast<const float2*>(gate + kGateEnd + 16 * ks + 8 * m + 2 * t);
                 xf[ks][2 * m] = pack_half2(ed.x * y[2 * ks + m][0], ed.y * y[2 * ks + m][1]);
                 xf[ks][2 * m + 1] = pack_half2(ed.x * y[2 * ks + m][2], ed.y * y[2 * ks + m][3]);
             }
-        const float d = gate[4 * kC];
+        const float d = gate[kGateAll];
 #pragma unroll
         for (int nt = 0; nt < 16; ++nt)
 #pragma unroll
@@ -275,7 +275,7 @@ __device__ void outputs(const GdrChunked& P, ChainSmem<NW>& S, const Span& span,
         }
 #pragma unroll
         for (int nt = 0; nt < 8; ++nt) {
-            const float2 e = *reinterpret_cast<const float2*>(gate + 2 * kC + 8 * nt + 2 * t);
+            const float2 e = *reinterpret_cast<const float2*>(gate + kGateE + 8 * nt + 2 * t);
             y[nt][0] *= e.x; y[nt][1] *= e.y; y[nt][2] *= e.x; y[nt][3] *= e.y;
         }
         if (!bar_wait(&S.x_full[w][buf], (unsigned)((c / 2) & 1), P.err)) return;
@@ -316,9 +316,33 @@ __device__ void outputs(const GdrChunked& P, ChainSmem<NW>& S, const Span& span,
     }
 }
 
+// For the backward pass: the output warps copy S^T and X^T of every chunk to memory instead.
+template <int NW>
+__device__ void keep(const GdrChunked& P, ChainSmem<NW>& S, const Span& span, int nch, int w, int lane, int h,
+                     int v0) {
+    for (int c = 0; c < nch; ++c) {
+        const int st = c % kStages, buf = c & 1;
+        auto& H = S.hand[w][buf];
+        const size_t at = (size_t)(span.chunk + c) * P.in.Hv + h;
+        if (!bar_wait(&S.s_full[w][buf], (unsigned)((c / 2) & 1), P.err)) return;
+        uint4* ds = reinterpret_cast<uint4*>(P.states + at * kStateTile + v0 * kDim * 2);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) ds[i * 32 + lane] = reinterpret_cast<const uint4*>(H.s)[i * 32 + lane];
+        if (!bar_wait(&S.x_full[w][buf], (unsigned)((c / 2) & 1), P.err)) return;
+        uint4* dx = reinterpret_cast<uint4*>(P.xs + at * kTokenTile + v0 * kC * 2);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) dx[i * 32 + lane] = reinterpret_cast<const uint4*>(H.x)[i * 32 + lane];
+        __syncwarp();
+        if (lane == 0) {
+            bar_arrive(&S.hand_empty[w][buf]);
+            bar_arrive(&S.empty[st]);
+        }
+    }
+}
+
 // One CTA per 16 NW value channels of a (sequence, value head): NW state warps, NW output
 // warps, 4 producer warps.
-template <int NW>
+template <int NW, bool kSave>
 __global__ void __launch_bounds__(64 * NW + kProducers, 1) gdr_chain_kernel(GdrChunked P) {
     extern __shared__ __align__(128) unsigned char raw[];
     ChainSmem<NW>& S = *reinterpret_cast<ChainSmem<NW>*>(raw);
@@ -347,18 +371,20 @@ __global__ void __launch_bounds__(64 * NW + kProducers, 1) gdr_chain_kernel(GdrC
     if (w < NW) {
         chain<NW>(P, S, nch, w, lane, sbase, part * 16 * NW + 16 * w);
     } else if (w < 2 * NW) {
-        outputs<NW>(P, S, span, nch, w - NW, lane, h, part * 16 * NW + 16 * (w - NW));
+        const int v0 = part * 16 * NW + 16 * (w - NW);
+        if (kSave) keep<NW>(P, S, span, nch, w - NW, lane, h, v0);
+        else outputs<NW>(P, S, span, nch, w - NW, lane, h, v0);
     } else if (nch > 0) {
-        produce<NW>(P, S, span, nch, h, part, tid - 64 * NW);
+        produce<NW, kSave>(P, S, span, nch, h, part, tid - 64 * NW);
     }
 }
 
-template <int NW>
+template <int NW, bool kSave>
 cudaError_t launch(const GdrChunked& P, cudaStream_t s) {
-    const cudaError_t e = allow_smem<gdr_chain_kernel<NW>>(sizeof(ChainSmem<NW>));
+    const cudaError_t e = allow_smem<gdr_chain_kernel<NW, kSave>>(sizeof(ChainSmem<NW>));
     if (e != cudaSuccess) return e;
     const long long ctas = (long long)P.in.N * P.in.Hv * (kDim / (16 * NW));
-    gdr_chain_kernel<NW><<<(unsigned)ctas, 64 * NW + kProducers, sizeof(ChainSmem<NW>), s>>>(P);
+    gdr_chain_kernel<NW, kSave><<<(unsigned)ctas, 64 * NW + kProducers, sizeof(ChainSmem<NW>), s>>>(P);
     return cudaGetLastError();
 }
 
@@ -367,7 +393,8 @@ cudaError_t launch(const GdrChunked& P, cudaStream_t s) {
 cudaError_t launch_gdr_chain(const GdrChunked& P, int sms, cudaStream_t s) {
     const long long units = (long long)P.in.N * P.in.Hv;
     if (units == 0) return cudaSuccess;
-    return units * 2 <= sms ? launch<2>(P, s) : launch<4>(P, s);
+    if (P.states) return units * 2 <= sms ? launch<2, true>(P, s) : launch<4, true>(P, s);
+    return units * 2 <= sms ? launch<2, false>(P, s) : launch<4, false>(P, s);
 }
 
 }  // namespace kda

@@ -31,10 +31,11 @@ namespace gdr {
 constexpr int kC = 64;                        // tokens per chunk
 // One (chunk, value head)'s block of scratch: T and P as fp16 [64][64] tiles (128-byte rows
 // whose 16-byte units are stored at unit ^ (row & 7)), then fp32 b, b e^G, e^G, e^(G_C - G)
-// of its 64 tokens and e^(G_C).
+// and G (in base 2) of its 64 tokens, and e^(G_C).
 constexpr int kTileBytes = kC * kC * 2;
-constexpr int kGateFloats = 4 * kC + 4;
-constexpr int kBlockUsed = 2 * kTileBytes + kGateFloats * 4;   // 17,424
+constexpr int kGateB = 0, kGateBe = kC, kGateE = 2 * kC, kGateEnd = 3 * kC, kGateG = 4 * kC, kGateAll = 5 * kC;
+constexpr int kGateFloats = 5 * kC + 4;
+constexpr int kBlockUsed = 2 * kTileBytes + kGateFloats * 4;   // 17,680
 constexpr int kBlockBytes = (kBlockUsed + 127) / 128 * 128;
 
 struct Chunks {           // where the chunks of each sequence are
@@ -51,6 +52,25 @@ struct Span {
 __device__ __forceinline__ Span span_of(const GdrInputs& I, const Chunks& C, int n) {
     if (I.cu) return {I.cu[n], I.cu[n + 1] - I.cu[n], C.first[n]};
     return {(long long)n * I.T, I.T, n * C.per_seq};
+}
+
+// Sequence and place of a chunk; false past the end of packed sequences (or for bad ones).
+__device__ __forceinline__ bool find_chunk(const GdrInputs& I, const Chunks& C, int chunk, int& n, int& c) {
+    if (!I.cu) {
+        n = chunk / C.per_seq;
+        c = chunk % C.per_seq;
+        return true;
+    }
+    if (!*I.valid || chunk >= C.first[I.N]) return false;
+    int lo = 0, hi = I.N;              // the last sequence whose first chunk is at most `chunk`
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (C.first[mid] <= chunk) lo = mid;
+        else hi = mid;
+    }
+    n = lo;
+    c = chunk - C.first[n];
+    return true;
 }
 
 // ---- mbarriers ----------------------------------------------------------------------
@@ -140,6 +160,22 @@ __device__ __forceinline__ uint32_t b_addr(uint32_t base, int r0, int u0, int la
     return unit_at<kRow>(base, r0 + (lane & 7) + ((lane >> 4) << 3), u0 + ((lane >> 3) & 1));
 }
 
+// What the backward pass keeps of each (chunk, value head): [128 value channels][128 key
+// channels] tiles of the state before the chunk (S^T) or of the gradient of the state after
+// it (dS^T), and [128][64] tiles of X^T or Y^T, fp16, 16-byte units swizzled as above.
+constexpr int kStateTile = kDim * kDim * 2;
+constexpr int kTokenTile = kDim * kC * 2;
+
+// Backward: the gradients that enter are scaled, per (sequence, key head), by the power of
+// two that brings the largest to 16 .. 32, so that fp16 operands keep their precision
+// whatever the loss is scaled by.  `amax` holds the bits of the largest magnitude.
+__device__ __forceinline__ float grad_scale(unsigned amax) {
+    const int e = (int)(amax >> 23);                // biased exponent of the largest
+    if (e == 0 || e == 255) return 1.0f;            // zero (or subnormal); not finite
+    const int x = 127 + 4 - (e - 127);              // 2^(4 - exponent)
+    return __uint_as_float((unsigned)(x < 1 ? 1 : x > 253 ? 253 : x) << 23);
+}
+
 }  // namespace gdr
 
 struct GdrChunked {       // a chunked forward pass
@@ -152,8 +188,28 @@ struct GdrChunked {       // a chunked forward pass
     void* final_state;                // or nullptr
     int final_dtype;
     int* err;
+    // backward pass: the forward pass keeps states and X instead of writing outputs
+    unsigned char* states = nullptr;  // [chunk][Hv] of kStateTile
+    unsigned char* xs = nullptr;      // [chunk][Hv] of kTokenTile
 };
 
+struct GdrBackward {      // what the backward pass has besides
+    GdrChunked fwd;
+    const __nv_bfloat16* dout;        // [tokens][Hv][128]
+    const void* dfinal;               // [N][Hv][128][128] or nullptr
+    int dfinal_dtype;
+    unsigned* amax;                   // [N][Hk]
+    unsigned char* dstates;           // [chunk][Hv] of kStateTile: gradient of the state after
+    unsigned char* ys;                // [chunk][Hv] of kTokenTile: Y^T
+    __nv_bfloat16 *dq, *dk, *dv;      // [tokens][heads][128]
+    void *dg, *dbeta;                 // [tokens][Hv] of the gates' type
+    void* dinit;                      // [N][Hv][128][128] of dinit_dtype or nullptr
+    int dinit_dtype;
+};
+
+cudaError_t launch_gdr_amax(const GdrBackward& P, cudaStream_t s);
+cudaError_t launch_gdr_bwd_chain(const GdrBackward& P, int sms, cudaStream_t s);
+cudaError_t launch_gdr_bwd_chunk(const GdrBackward& P, cudaStream_t s);
 cudaError_t launch_gdr_map(const GdrInputs& in, int* first, int* valid, int* err, cudaStream_t s);
 cudaError_t launch_gdr_prep(const GdrChunked& P, cudaStream_t s);
 cudaError_t launch_gdr_chain(const GdrChunked& P, int sms, cudaStream_t s);

@@ -128,20 +128,7 @@ __global__ void __launch_bounds__(kPrepThreads) gdr_prep_kernel(GdrChunked P) {
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, g = lane >> 2, t = lane & 3;
     const int chunk = blockIdx.x, hk = blockIdx.y;
     int n, c;
-    if (I.cu) {
-        if (!*I.valid || chunk >= P.chunks.first[I.N]) return;
-        int lo = 0, hi = I.N;          // the last sequence whose first chunk is at most `chunk`
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) / 2;
-            if (P.chunks.first[mid] <= chunk) lo = mid;
-            else hi = mid;
-        }
-        n = lo;
-        c = chunk - P.chunks.first[n];
-    } else {
-        n = chunk / P.chunks.per_seq;
-        c = chunk % P.chunks.per_seq;
-    }
+    if (!find_chunk(I, P.chunks, chunk, n, c)) return;
     const Span span = span_of(I, P.chunks, n);
     const long long tok = span.start + (long long)c * kC;
     const int rows = min(kC, span.len - c * kC);
@@ -205,11 +192,12 @@ __global__ void __launch_bounds__(kPrepThreads) gdr_prep_kernel(GdrChunked P) {
             S.b[2 * lane + 1] = b1;
             float* gates = reinterpret_cast<float*>(block + 2 * kTileBytes);
             const float e0 = ex2_approx(x0), e1 = ex2_approx(x);
-            reinterpret_cast<float2*>(gates)[lane] = make_float2(b0, b1);
-            reinterpret_cast<float2*>(gates + kC)[lane] = make_float2(b0 * e0, b1 * e1);
-            reinterpret_cast<float2*>(gates + 2 * kC)[lane] = make_float2(e0, e1);
-            reinterpret_cast<float2*>(gates + 3 * kC)[lane] = make_float2(ex2_approx(last - x0), ex2_approx(last - x));
-            if (lane == 0) gates[4 * kC] = ex2_approx(last);
+            reinterpret_cast<float2*>(gates + kGateB)[lane] = make_float2(b0, b1);
+            reinterpret_cast<float2*>(gates + kGateBe)[lane] = make_float2(b0 * e0, b1 * e1);
+            reinterpret_cast<float2*>(gates + kGateE)[lane] = make_float2(e0, e1);
+            reinterpret_cast<float2*>(gates + kGateEnd)[lane] = make_float2(ex2_approx(last - x0), ex2_approx(last - x));
+            reinterpret_cast<float2*>(gates + kGateG)[lane] = make_float2(x0, x);
+            if (lane == 0) gates[kGateAll] = ex2_approx(last);
         }
         __syncthreads();
         // A in fp32 and P in fp16

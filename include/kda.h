@@ -411,12 +411,45 @@ int kda_qk_norm_bwd(const void* q, const void* k, const void* dq_out, const void
  *   initial_state, final_state, cu_seqlens, num_seqs   as kda_fwd: [N, Hv, 128, 128], row =
  *               key channel, or NULL; a malformed cu_seqlens writes nothing
  *   B >= 1, T >= 0, K = V = 128
+ *
+ * The state is carried in fp32; the tensor-core products have fp16 operands, so q, k, v and
+ * the states have to stay below 65,504 in magnitude.  Takes about 0.3 KB of scratch per
+ * token and value head from the stream-ordered allocator.  Deterministic.
  */
 int kda_gdr_fwd(const void* q, const void* k, const void* v, const void* g, const void* beta,
                 int gate_dtype, float scale, void* out, const void* initial_state,
                 int initial_state_dtype, void* final_state, int final_state_dtype,
                 const int32_t* cu_seqlens, int num_seqs, int B, int T, int Hk, int Hv, int K, int V,
                 long long q_stride, long long k_stride, long long v_stride, void* stream);
+
+/*
+ * kda_gdr_bwd -- the backward pass of kda_gdr_fwd: gradients of a scalar loss L with respect
+ * to its inputs, given dL/d(out) and, optionally, dL/d(final state).
+ *
+ *   inputs      as kda_gdr_fwd
+ *   d_out       bf16 [B, T, Hv, 128], contiguous
+ *   d_final_state  [N, Hv, 128, 128] of d_final_state_dtype, or NULL (zero)
+ *   dq, dk      bf16 [B, T, Hk, 128], contiguous, summed over the value heads of a group
+ *   dv          bf16 [B, T, Hv, 128]; dg, dbeta [B, T, Hv] of gate_dtype
+ *   d_initial_state  [N, Hv, 128, 128] of d_initial_state_dtype, or NULL (not written)
+ *
+ * The forward pass's states are formed again.  Accuracy is that of fp16 operands with fp32
+ * sums, whatever the gates' type: the incoming gradients are scaled per (sequence, key head)
+ * by the power of two that brings the largest to 16 .. 32, so gradients of any size keep it;
+ * q, k, v and the states have to stay below 65,504 as in kda_gdr_fwd.  Deterministic.
+ * Scratch: kda_gdr_bwd_workspace_bytes() from the stream-ordered allocator (about 1.8 KB per
+ * token and value head).
+ */
+int kda_gdr_bwd(const void* q, const void* k, const void* v, const void* g, const void* beta,
+                int gate_dtype, float scale, const void* initial_state, int initial_state_dtype,
+                const void* d_out, const void* d_final_state, int d_final_state_dtype, void* dq,
+                void* dk, void* dv, void* dg, void* dbeta, void* d_initial_state,
+                int d_initial_state_dtype, const int32_t* cu_seqlens, int num_seqs, int B, int T,
+                int Hk, int Hv, int K, int V, long long q_stride, long long k_stride,
+                long long v_stride, void* stream);
+
+/* Bytes of scratch kda_gdr_bwd takes from the stream-ordered allocator (host-only). */
+size_t kda_gdr_bwd_workspace_bytes(int B, int T, int Hk, int Hv, int num_seqs, int varlen);
 
 /*
  * kda_gdr_step -- the rule for T new tokens (one, or a few drafted ones) of each of N
@@ -494,7 +527,10 @@ enum {
     KDA_KERNEL_GDR_MAP = 14,
     KDA_KERNEL_GDR_PREP = 15,
     KDA_KERNEL_GDR_CHAIN = 16,
-    KDA_NUM_KERNELS = 17
+    KDA_KERNEL_GDR_AMAX = 17,
+    KDA_KERNEL_GDR_BWD_CHAIN = 18,
+    KDA_KERNEL_GDR_BWD_CHUNK = 19,
+    KDA_NUM_KERNELS = 20
 };
 int kda_profile_enable(int on);
 int kda_profile_read(double* total_ms, long long* launches);
