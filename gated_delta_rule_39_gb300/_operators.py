@@ -4,6 +4,7 @@ passes): argument checks and marshalling, as in the package's other calls."""
 from __future__ import annotations
 
 import ctypes
+import sys
 
 _vp, _i, _f, _ll = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_longlong
 _NORMS = {"l2": 0, "rms": 1}
@@ -29,16 +30,23 @@ def declare(lib):
     return lib
 
 
+# The checks below run on every call, where a decode step's whole kernel takes a few
+# microseconds, so they read each attribute of a tensor once and import nothing.
+def _torch():
+    """The torch module: loaded already wherever a tensor has been made."""
+    return sys.modules["torch"]
+
+
 def _call(name, device, stream, *args):
     """One library call on `device` and `stream` (default: the current stream)."""
-    import torch
-
-    import gated_delta_rule_39_gb300 as kda
-    fn = getattr(kda.load_library(), name)
+    torch, kda = _torch(), sys.modules[__package__]
+    fn = getattr(kda._lib or kda.load_library(), name)
+    index = device.index
     if stream is None:
-        stream = torch.cuda.current_stream(device)
-    s = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-    if torch.cuda.current_device() == device.index:
+        s = torch._C._cuda_getCurrentRawStream(index)
+    else:
+        s = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    if torch.cuda.current_device() == index:
         rc = fn(*args, s)
     else:
         with torch.cuda.device(device):
@@ -52,9 +60,10 @@ def _ptr(t):
 
 
 def _cuda(t, where):
-    if t.device.type != "cuda":
+    device = t.device
+    if device.type != "cuda":
         raise ValueError(f"{where} takes CUDA tensors")
-    return t.device
+    return device
 
 
 def _is(t, name, dtypes, shape, device):
@@ -70,25 +79,28 @@ def _is(t, name, dtypes, shape, device):
 
 
 def _dense(t, name, dtypes, shape, device):
+    if t is None:
+        return
     _is(t, name, dtypes, shape, device)
-    if t is not None and not t.is_contiguous():
+    if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
 
 
 def _token_stride(t, name):
     """Elements from one token to the next of [..., heads, channels], whose tokens must be
     equally spaced and whose heads and channels contiguous."""
-    h, d = t.shape[-2], t.shape[-1]
+    shape, s = t.shape, t.stride()
+    h, d = shape[-2], shape[-1]
     if t.is_contiguous():
         return h * d
-    s = t.stride()
     ok = (d == 1 or s[-1] == 1) and (h == 1 or s[-2] == d)
     step, span = None, 1
-    for size, stride in zip(reversed(t.shape[:-2]), reversed(s[:-2])):
-        if size != 1:
-            step = stride if step is None else step
-            ok = ok and stride == step * span
-            span *= size
+    for i in range(len(s) - 3, -1, -1):
+        if shape[i] != 1:
+            if step is None:
+                step = s[i]
+            ok = ok and s[i] == step * span
+            span *= shape[i]
     if not ok or (step is not None and step < h * d):
         raise ValueError(f"{name}: heads and channels must be contiguous and tokens equally spaced, "
                          f"got strides {s}")
@@ -96,21 +108,22 @@ def _token_stride(t, name):
 
 
 def _norm_args(where, q, k, norm, q_weight, k_weight, cos, sin, positions):
-    import torch
-    dev = _cuda(q, where)
-    types = (torch.bfloat16, torch.float32)
-    if q.dim() < 3 or k.shape[:-2] != q.shape[:-2] or k.shape[-1] != q.shape[-1]:
+    torch = _torch()
+    dev, qs, ks, dtype = _cuda(q, where), q.shape, k.shape, q.dtype
+    if len(qs) < 3 or ks[:-2] != qs[:-2] or ks[-1] != qs[-1]:
         raise ValueError(f"q and k must be [..., heads, channels] with the same tokens and "
-                         f"channels, got {tuple(q.shape)} and {tuple(k.shape)}")
-    _is(q, "q", types, q.shape, dev)
-    _is(k, "k", (q.dtype,), k.shape, dev)
+                         f"channels, got {tuple(qs)} and {tuple(ks)}")
+    if dtype is not torch.bfloat16 and dtype is not torch.float32:
+        raise TypeError(f"q must be torch.bfloat16 or torch.float32, got {dtype}")
+    _is(k, "k", (dtype,), ks, dev)
     if norm not in _NORMS:
         raise ValueError(f"norm must be 'l2' or 'rms', got {norm!r}")
-    D = q.shape[-1]
+    D = qs[-1]
     f32 = (torch.float32,)
-    _dense(q_weight, "q_weight", f32, (D,), dev)
-    _dense(k_weight, "k_weight", f32, (D,), dev)
-    T = q.shape[:-2].numel()
+    if q_weight is not None:
+        _dense(q_weight, "q_weight", f32, (D,), dev)
+    if k_weight is not None:
+        _dense(k_weight, "k_weight", f32, (D,), dev)
     rows = rotary = 0
     if cos is not None:
         if sin is None or cos.dim() != 2 or 2 * cos.shape[1] > D:
@@ -118,13 +131,14 @@ def _norm_args(where, q, k, norm, q_weight, k_weight, cos, sin, positions):
         rows, rotary = cos.shape[0], 2 * cos.shape[1]
         _dense(cos, "cos", f32, cos.shape, dev)
         _dense(sin, "sin", f32, cos.shape, dev)
-        _dense(positions, "positions", (torch.int32,), q.shape[:-2], dev)
+        _dense(positions, "positions", (torch.int32,), qs[:-2], dev)
     elif sin is not None or positions is not None:
         raise ValueError("sin and positions need cos")
     head = (_ptr(q_weight), _ptr(k_weight))
     tail = (_ptr(cos), _ptr(sin), _ptr(positions), rows, rotary)
-    sizes = (T, q.shape[-2], k.shape[-2], D, _token_stride(q, "q"), _token_stride(k, "k"))
-    return dev, int(q.dtype == torch.float32), head, tail, sizes
+    tokens = qs[0] if len(qs) == 3 else qs[:-2].numel()
+    sizes = (tokens, qs[-2], ks[-2], D, _token_stride(q, "q"), _token_stride(k, "k"))
+    return dev, int(dtype is torch.float32), head, tail, sizes
 
 
 def kda_qk_norm(q, k, q_out, k_out, norm: str = "l2", eps: float = 1e-6, q_weight=None,
@@ -153,7 +167,7 @@ def kda_qk_norm_bwd(q, k, dq_out, dk_out, norm: str = "l2", eps: float = 1e-6, q
                     stream=None) -> dict:
     """Gradients of ``kda_qk_norm`` from dL/d(q_out) and dL/d(k_out) (contiguous, of q's
     type): dq, dk (contiguous, of q's type) and, with weights, dq_weight, dk_weight (fp32 [D])."""
-    import torch
+    torch = _torch()
     dev, f32, w, turn, sizes = _norm_args("kda_qk_norm_bwd", q, k, norm, q_weight, k_weight, cos, sin,
                                           positions)
     _dense(dq_out, "dq_out", (q.dtype,), q.shape, dev)
@@ -171,36 +185,39 @@ def kda_qk_norm_bwd(q, k, dq_out, dk_out, norm: str = "l2", eps: float = 1e-6, q
 
 
 def _rule_args(where, q, k, v, g, beta):
-    import torch
-    dev = _cuda(q, where)
+    torch = _torch()
+    dev, qs, vs = _cuda(q, where), q.shape, v.shape
     bf16 = (torch.bfloat16,)
-    if q.dim() != 4 or v.dim() != 4:
+    if len(qs) != 4 or len(vs) != 4:
         raise ValueError("q, k and v must be [B, T, heads, 128]")
-    B, T, Hk, K = q.shape
-    Hv, V = v.shape[2], v.shape[3]
-    _is(q, "q", bf16, q.shape, dev)
-    _is(k, "k", bf16, q.shape, dev)
+    B, T, Hk, K = qs
+    Hv, V = vs[2], vs[3]
+    _is(q, "q", bf16, qs, dev)
+    _is(k, "k", bf16, qs, dev)
     _is(v, "v", bf16, (B, T, Hv, V), dev)
-    gates = (torch.float32, torch.bfloat16)
-    _dense(g, "g", gates, (B, T, Hv), dev)
-    _dense(beta, "beta", (g.dtype,), (B, T, Hv), dev)
-    head = (_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), int(g.dtype == torch.float32))
+    gate = g.dtype
+    _dense(g, "g", (torch.float32, torch.bfloat16), (B, T, Hv), dev)
+    _dense(beta, "beta", (gate,), (B, T, Hv), dev)
+    head = (q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), int(gate is torch.float32))
     strides = (_token_stride(q, "q"), _token_stride(k, "k"), _token_stride(v, "v"))
     return dev, head, (B, T, Hk, Hv, K, V), strides
 
 
 def _states(dev, shape, **states):
-    import torch
+    torch = _torch()
     r = []
     for name, t in states.items():
-        _dense(t, name, (torch.float32, torch.bfloat16), shape, dev)
-        r += [_ptr(t), int(t is not None and t.dtype == torch.float32)]
+        if t is None:
+            r += (None, 0)
+        else:
+            _dense(t, name, (torch.float32, torch.bfloat16), shape, dev)
+            r += (t.data_ptr(), int(t.dtype is torch.float32))
     return r
 
 
 def _sequences(cu_seqlens, B, dev):
     """(number of states, the C call's num_seqs) of a call."""
-    import torch
+    torch = _torch()
     if cu_seqlens is None:
         return B, 0
     if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
@@ -219,7 +236,7 @@ def kda_gdr_fwd(q, k, v, g, beta, scale: float, out, initial_state=None, final_s
     strength): fp32 or bf16 [B, T, Hv]; states: optional bf16 or fp32 [N, Hv, 128, 128];
     cu_seqlens: optional int32 [N + 1] (then B == 1).  Raises KdaError on a rejected call.
     """
-    import torch
+    torch = _torch()
     dev, head, (B, T, Hk, Hv, K, V), strides = _rule_args("kda_gdr_fwd", q, k, v, g, beta)
     _dense(out, "out", (torch.bfloat16,), (B, T, Hv, V), dev)
     N, num = _sequences(cu_seqlens, B, dev)
@@ -238,7 +255,7 @@ def kda_gdr_bwd(q, k, v, g, beta, scale: float, d_out, initial_state=None, d_fin
     (bf16 [B, T, Hk, 128]), dv (bf16 [B, T, Hv, 128]), dg, dbeta ([B, T, Hv] of the gates' type)
     and, with an initial state (unless d_initial_state is False), d_initial_state of its type.
     """
-    import torch
+    torch = _torch()
     dev, head, (B, T, Hk, Hv, K, V), strides = _rule_args("kda_gdr_bwd", q, k, v, g, beta)
     _dense(d_out, "d_out", (torch.bfloat16,), (B, T, Hv, V), dev)
     N, num = _sequences(cu_seqlens, B, dev)
@@ -259,8 +276,7 @@ def kda_gdr_bwd(q, k, v, g, beta, scale: float, d_out, initial_state=None, d_fin
 
 def kda_gdr_bwd_workspace_bytes(B: int, T: int, Hk: int, Hv: int, num_seqs: int = 0,
                                 varlen: bool = False) -> int:
-    import gated_delta_rule_39_gb300 as kda
-    return int(kda.load_library().kda_gdr_bwd_workspace_bytes(B, T, Hk, Hv, num_seqs, int(varlen)))
+    return int(sys.modules[__package__].load_library().kda_gdr_bwd_workspace_bytes(B, T, Hk, Hv, num_seqs, int(varlen)))
 
 
 def kda_gdr_step(q, k, v, g, beta, scale: float, out=None, state_in=None, state_out=None,
@@ -274,7 +290,7 @@ def kda_gdr_step(q, k, v, g, beta, scale: float, out=None, state_in=None, state_
     sequence's state (-1: a padding entry); lengths: optional int32 [N], the tokens after
     which the state is kept (default T).  Raises KdaError on a rejected call.
     """
-    import torch
+    torch = _torch()
     dev, head, (N, T, Hk, Hv, K, V), strides = _rule_args("kda_gdr_step", q, k, v, g, beta)
     _dense(out, "out", (torch.bfloat16,), (N, T, Hv, V), dev)
     pool = N
@@ -300,7 +316,7 @@ def kda_verify_drafts(target_probs, draft_probs, draft_tokens, uniform, noise, a
     and tokens (int32 [N, D + 1]: the kept drafts, the next token, then -1).
     Raises KdaError on a rejected call.
     """
-    import torch
+    torch = _torch()
     dev = _cuda(target_probs, "kda_verify_drafts")
     if target_probs.dim() != 3 or target_probs.shape[1] < 1:
         raise ValueError("target_probs must be [N, D + 1, V]")
