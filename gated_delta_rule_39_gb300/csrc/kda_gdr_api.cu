@@ -64,17 +64,18 @@ size_t plan_chunks(bool varlen, int B, int T, int N, gdr::Chunks* c) {
 }
 
 // Scratch of a backward pass (bytes from its start): the map of packed sequences, the
-// largest gradients, and per (chunk, value head) a block, S^T, X^T, dS^T and Y^T.
+// largest gradients, and per (chunk, value head) a block, T, S^T, X^T, dS^T and Y^T.
 struct BwdLayout {
     gdr::Chunks chunks{};
-    size_t amax, blocks, states, xs, dstates, ys, total;
+    size_t amax, blocks, ts, states, xs, dstates, ys, total;
 };
 BwdLayout bwd_layout(bool varlen, int B, int T, int Hk, int Hv, int N) {
     BwdLayout L{};
     L.amax = plan_chunks(varlen, B, T, N, &L.chunks);
     const size_t units = (size_t)L.chunks.total * Hv;
     L.blocks = L.amax + align_up((size_t)N * Hk * 4);
-    L.states = L.blocks + units * gdr::kBlockBytes;
+    L.ts = L.blocks + units * gdr::kBlockBytes;
+    L.states = L.ts + units * gdr::kTileBytes;
     L.xs = align_up(L.states + units * gdr::kStateTile);
     L.dstates = L.xs + units * gdr::kTokenTile;
     L.ys = L.dstates + units * gdr::kStateTile;
@@ -160,8 +161,8 @@ int kda_gdr_fwd(const void* q, const void* k, const void* v, const void* g, cons
         overlaps(out, n_out, cu_seqlens, ((size_t)N + 1) * 4) ||
         overlaps(final_state, n_so, cu_seqlens, ((size_t)N + 1) * 4))
         return KDA_ERR_ALIAS;
-    int dev = 0, sms = 0;
-    rc = device_setup(&dev, &P.err, &sms);
+    int dev = 0;
+    rc = device_setup(&dev, &P.err);
     if (rc != KDA_OK) return rc;
     P.out = static_cast<__nv_bfloat16*>(out);
     P.init_state = initial_state;
@@ -184,7 +185,7 @@ int kda_gdr_fwd(const void* q, const void* k, const void* v, const void* g, cons
     }
     if (e == cudaSuccess) e = timed_launch(KDA_KERNEL_GDR_PREP, s, [&] { return launch_gdr_prep(P, s); });
     if (e == cudaSuccess)
-        e = timed_launch(KDA_KERNEL_GDR_CHAIN, s, [&] { return launch_gdr_chain(P, sms, s); });
+        e = timed_launch(KDA_KERNEL_GDR_CHAIN, s, [&] { return launch_gdr_chain(P, s); });
     cudaFreeAsync(scratch, s);
     if (e != cudaSuccess) return cuda_fail(KDA_ERR_LAUNCH, e);
     return KDA_OK;
@@ -236,8 +237,8 @@ int kda_gdr_bwd(const void* q, const void* k, const void* v, const void* g, cons
         for (int o2 = o + 1; o2 < 6; ++o2)
             if (overlaps(out_p[o], out_n[o], out_p[o2], out_n[o2])) return KDA_ERR_ALIAS;
     }
-    int dev = 0, sms = 0;
-    rc = device_setup(&dev, &P.fwd.err, &sms);
+    int dev = 0;
+    rc = device_setup(&dev, &P.fwd.err);
     if (rc != KDA_OK) return rc;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const BwdLayout L = bwd_layout(varlen, B, T, Hk, Hv, N);
@@ -246,6 +247,7 @@ int kda_gdr_bwd(const void* q, const void* k, const void* v, const void* g, cons
     if (e != cudaSuccess) return cuda_fail(KDA_ERR_ALLOC, e);
     P.fwd.chunks = L.chunks;
     P.fwd.blocks = scratch + L.blocks;
+    P.fwd.ts = scratch + L.ts;
     P.fwd.init_state = initial_state;
     P.fwd.init_dtype = initial_state_dtype;
     P.fwd.states = scratch + L.states;
@@ -274,9 +276,7 @@ int kda_gdr_bwd(const void* q, const void* k, const void* v, const void* g, cons
     if (e == cudaSuccess) e = timed_launch(KDA_KERNEL_GDR_AMAX, s, [&] { return launch_gdr_amax(P, s); });
     if (e == cudaSuccess) e = timed_launch(KDA_KERNEL_GDR_PREP, s, [&] { return launch_gdr_prep(P.fwd, s); });
     if (e == cudaSuccess)
-        e = timed_launch(KDA_KERNEL_GDR_CHAIN, s, [&] { return launch_gdr_chain(P.fwd, sms, s); });
-    if (e == cudaSuccess)
-        e = timed_launch(KDA_KERNEL_GDR_BWD_CHAIN, s, [&] { return launch_gdr_bwd_chain(P, sms, s); });
+        e = timed_launch(KDA_KERNEL_GDR_BWD_CHAIN, s, [&] { return launch_gdr_bwd_chain(P, s); });
     if (e == cudaSuccess)
         e = timed_launch(KDA_KERNEL_GDR_BWD_CHUNK, s, [&] { return launch_gdr_bwd_chunk(P, s); });
     cudaFreeAsync(scratch, s);

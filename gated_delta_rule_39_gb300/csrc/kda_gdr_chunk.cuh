@@ -5,32 +5,32 @@
 // j <= i, A the strictly lower triangle of beta_i M_ij k_i.k_j, T = (I + A)^-1 and S the
 // state before it,
 //
-//   R = beta (V - e^G K S),  X = T R          (row j of X is the update d_j)
+//   R = V - e^G K S,  X = T beta R            (row j of X is the update d_j)
 //   O = scale (e^G Q S + (M . Q K^T) X)
-//   S <- e^(G_C) S + K^T (e^(G_C - G) X)
+//   S <- e^(G_C) S + (e^(G_C - G) K)^T X
 //
 // T and P = M . Q K^T depend on queries, keys and gates alone: the prep kernel forms
 // them for all chunks in parallel; the chain kernel then walks the chunks of a sequence.
 //
 // Numerics: G, the decays and every product's accumulator are fp32, and so is the state
 // between chunks.  The operands of the tensor-core products are fp16: queries, keys (bf16
-// data, exact in fp16 for magnitudes of 2^-14 to 65,504), T, P, R, X and the rounded state.
-// fp16's 11 bits keep the result within 4e-4 of the exact one on unit keys, where bf16
+// data) times their decays, T beta, P, R, X and the rounded state.
+// fp16's 11 bits keep the result within 5e-4 of the exact one on unit keys, where bf16
 // operands gave 3e-3; its price is that keys, queries, values and states have to stay
 // below 65,504.  The inverse T is formed in fp32 with tf32 products between its blocks.
 #pragma once
 #include "kda_gdr.cuh"
 
-#ifndef KDA_SPIN_LIMIT
-#define KDA_SPIN_LIMIT (1LL << 32)   // cycles that a wait inside a kernel may take (about 2 s)
+#ifndef KDA_WAIT_TRIES
+#define KDA_WAIT_TRIES (1u << 20)    // of a wait inside a kernel (a fraction of a second to 20 s)
 #endif
 
 namespace kda {
 namespace gdr {
 
 constexpr int kC = 64;                        // tokens per chunk
-// One (chunk, value head)'s block of scratch: T and P as fp16 [64][64] tiles (128-byte rows
-// whose 16-byte units are stored at unit ^ (row & 7)), then fp32 b, b e^G, e^G, e^(G_C - G)
+// One (chunk, value head)'s block of scratch: T beta (columns scaled) and P as fp16 [64][64]
+// tiles (128-byte rows whose 16-byte units are stored at unit ^ (row & 7)), then fp32 b, b e^G, e^G, e^(G_C - G)
 // and G (in base 2) of its 64 tokens, and e^(G_C).
 constexpr int kTileBytes = kC * kC * 2;
 constexpr int kGateB = 0, kGateBe = kC, kGateE = 2 * kC, kGateEnd = 3 * kC, kGateG = 4 * kC, kGateAll = 5 * kC;
@@ -80,27 +80,27 @@ __device__ __forceinline__ void bar_init(uint64_t* b, int count) {
 __device__ __forceinline__ void bar_arrive(uint64_t* b) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(smem_u32(b)) : "memory");
 }
-// arrives once the thread's earlier cp.async copies have landed
-__device__ __forceinline__ void bar_arrive_copies(uint64_t* b) {
-    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];\n" ::"r"(smem_u32(b)) : "memory");
+// a 16-byte copy that is a zero where `there` is false
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool there) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
 }
-// Waits, as a whole warp, for a phase to end; after KDA_SPIN_LIMIT cycles records a timeout
-// and gives up (every lane gets the same answer).
+__device__ __forceinline__ void copies_landed() { asm volatile("cp.async.wait_all;\n" ::: "memory"); }
+// Waits, as a whole warp, for a phase to end; after KDA_WAIT_TRIES tries (each of which sleeps
+// for up to 20 us, as the hardware sees fit) records a timeout and gives up.  Every lane gets
+// the same answer.  Kept short: it is part of every role's loop.
 __device__ __forceinline__ bool bar_wait(uint64_t* b, unsigned parity, int* err) {
-    const long long t0 = clock64();
-    for (;;) {
+#pragma unroll 1
+    for (unsigned n = 0; n < KDA_WAIT_TRIES; ++n) {
         unsigned ok;
         asm volatile(
             "{\n .reg .pred p;\n"
-            " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+            " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 20000;\n"
             " selp.u32 %0, 1, 0, p;\n}\n"
             : "=r"(ok) : "r"(smem_u32(b)), "r"(parity) : "memory");
         if (__all_sync(0xFFFFFFFFu, ok)) return true;
-        if (__any_sync(0xFFFFFFFFu, clock64() - t0 > KDA_SPIN_LIMIT)) {
-            set_error(err, KDA_ERR_DEVICE_TIMEOUT);
-            return false;
-        }
     }
+    set_error(err, KDA_ERR_DEVICE_TIMEOUT);
+    return false;
 }
 
 // ---- fragments --------------------------------------------------------------------------
@@ -160,14 +160,17 @@ __device__ __forceinline__ uint32_t b_addr(uint32_t base, int r0, int u0, int la
     return unit_at<kRow>(base, r0 + (lane & 7) + ((lane >> 4) << 3), u0 + ((lane >> 3) & 1));
 }
 
-// What the backward pass keeps of each (chunk, value head): [128 value channels][128 key
-// channels] tiles of the state before the chunk (S^T) or of the gradient of the state after
-// it (dS^T), and [128][64] tiles of X^T or Y^T, fp16, 16-byte units swizzled as above.
+// What the backward pass keeps of each (chunk, value head), in fp16: S^T before the chunk (128
+// value channels x 128 key channels) and the gradient of the state after it (dS^T), X^T and
+// Y^T (128 x 64 tokens), T.  Rows are value channels; the 16-byte unit u of row v is at
+// (128 u + v) * 16, so that a warp whose lanes are rows writes 512 consecutive bytes, and 8
+// rows of an ldmatrix are 128 consecutive ones.
+__device__ __forceinline__ int row_unit(int v, int u) { return (128 * u + v) * 16; }
 constexpr int kStateTile = kDim * kDim * 2;
 constexpr int kTokenTile = kDim * kC * 2;
 
-// Backward: the gradients that enter are scaled, per (sequence, key head), by the power of
-// two that brings the largest to 16 .. 32, so that fp16 operands keep their precision
+// Backward: the gradients that enter (scale dO, and that of the last state) are scaled, per
+// (sequence, key head), by the power of two that brings the largest to 16 .. 32, so that fp16 operands keep their precision
 // whatever the loss is scaled by.  `amax` holds the bits of the largest magnitude.
 __device__ __forceinline__ float grad_scale(unsigned amax) {
     const int e = (int)(amax >> 23);                // biased exponent of the largest
@@ -191,6 +194,7 @@ struct GdrChunked {       // a chunked forward pass
     // backward pass: the forward pass keeps states and X instead of writing outputs
     unsigned char* states = nullptr;  // [chunk][Hv] of kStateTile
     unsigned char* xs = nullptr;      // [chunk][Hv] of kTokenTile
+    unsigned char* ts = nullptr;      // [chunk][Hv] of kTileBytes: T without beta
 };
 
 struct GdrBackward {      // what the backward pass has besides
@@ -208,10 +212,10 @@ struct GdrBackward {      // what the backward pass has besides
 };
 
 cudaError_t launch_gdr_amax(const GdrBackward& P, cudaStream_t s);
-cudaError_t launch_gdr_bwd_chain(const GdrBackward& P, int sms, cudaStream_t s);
+cudaError_t launch_gdr_bwd_chain(const GdrBackward& P, cudaStream_t s);
 cudaError_t launch_gdr_bwd_chunk(const GdrBackward& P, cudaStream_t s);
 cudaError_t launch_gdr_map(const GdrInputs& in, int* first, int* valid, int* err, cudaStream_t s);
 cudaError_t launch_gdr_prep(const GdrChunked& P, cudaStream_t s);
-cudaError_t launch_gdr_chain(const GdrChunked& P, int sms, cudaStream_t s);
+cudaError_t launch_gdr_chain(const GdrChunked& P, cudaStream_t s);
 
 }  // namespace kda

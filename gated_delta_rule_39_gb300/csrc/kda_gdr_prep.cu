@@ -1,6 +1,6 @@
 // Chunk-parallel part of the gated delta rule with one decay per value head: where the
-// chunks of packed sequences are (map), and each chunk's T = (I + A)^-1, P = M . Q K^T and
-// decays (prep).
+// chunks of packed sequences are (map), and each chunk's T = (I + A)^-1 (times beta), P =
+// M . Q K^T and decays (prep).
 #include "kda_gdr_chunk.cuh"
 
 namespace kda {
@@ -54,16 +54,26 @@ __global__ void __launch_bounds__(kMapThreads) gdr_map_kernel(GdrInputs I, int* 
 // K K^T and Q K^T on tensor cores (bf16 data, fp32 sums; kept in registers for all value
 // heads of the group), and per value head: the gates' running sum, A and P, and
 // T = (I + A)^-1: the four 16 x 16 diagonal blocks by forward substitution in fp32 (a lane
-// owns a column), then T21 = -T22 A21 T11 for blocks of 16 and of 32 with tf32 products.
+// owns a column), then T21 = -T22 A21 T11 for blocks of 16 and of 32 with tf32 products.  T
+// takes A's place block by block.
+//
+// Bound by memory (K and Q once, 16 KB of T and P out per value head) once enough CTAs share
+// an SM to cover each other's chains of small steps: A, T and P live where K and Q were.
 constexpr int kPrepThreads = 128;
-constexpr int kLd = 68;               // row length of the fp32 tiles: rows 4 banks apart
+constexpr int kLd = 68;               // row length of the fp32 tile: rows 4 banks apart
 
 struct PrepSmem {
-    __align__(128) unsigned char k[kC * kDim * 2];
-    __align__(128) unsigned char q[kC * kDim * 2];     // later: P as fp16
-    __align__(16) float a[kC][kLd];                    // A (strictly lower)
-    __align__(16) float t[kC][kLd];                    // T (lower blocks)
-    float g[kC];                                       // running sum of g in base 2
+    union {
+        struct {
+            __align__(128) unsigned char k[kC * kDim * 2];
+            __align__(128) unsigned char q[kC * kDim * 2];
+        };
+        struct {
+            __align__(16) float a[kC][kLd];                // A (strictly lower), then T
+            __align__(128) unsigned char p[kTileBytes];    // P as fp16
+        };
+    };
+    float g[kC];                                           // running sum of g in base 2
     float b[kC];
 };
 
@@ -80,62 +90,88 @@ __device__ __forceinline__ void load_tile(uint32_t dst, const __nv_bfloat16* src
     }
 }
 
-// C(16 x 8 kN) = A(rows ar .., cols ac ..) B(rows br .., cols bc ..), 8 kK deep, from fp32 tiles
+// F(16 x 8 kN) = M(rows ar .., cols ac ..) M(rows br .., cols bc ..), 8 kK deep
 template <int kN, int kK>
-__device__ __forceinline__ void tf32_product(float (&c)[kN][4], const float (*A)[kLd], int ar, int ac,
-                                             const float (*B)[kLd], int br, int bc, int lane) {
+__device__ __forceinline__ void tf32_product(float (&c)[kN][4], const float (*M)[kLd], int ar, int ac, int br, int bc,
+                                             int lane) {
     const int g = lane >> 2, t = lane & 3;
 #pragma unroll
     for (int n = 0; n < kN; ++n) c[n][0] = c[n][1] = c[n][2] = c[n][3] = 0.0f;
 #pragma unroll
     for (int k = 0; k < kK; ++k) {
-        const uint32_t a[4] = {tf32_bits(A[ar + g][ac + 8 * k + t]), tf32_bits(A[ar + g + 8][ac + 8 * k + t]),
-                               tf32_bits(A[ar + g][ac + 8 * k + t + 4]),
-                               tf32_bits(A[ar + g + 8][ac + 8 * k + t + 4])};
+        const uint32_t a[4] = {tf32_bits(M[ar + g][ac + 8 * k + t]), tf32_bits(M[ar + g + 8][ac + 8 * k + t]),
+                               tf32_bits(M[ar + g][ac + 8 * k + t + 4]),
+                               tf32_bits(M[ar + g + 8][ac + 8 * k + t + 4])};
 #pragma unroll
         for (int n = 0; n < kN; ++n)
-            mma_tf32(c[n], a, tf32_bits(B[br + 8 * k + t][bc + 8 * n + g]),
-                     tf32_bits(B[br + 8 * k + t + 4][bc + 8 * n + g]));
+            mma_tf32(c[n], a, tf32_bits(M[br + 8 * k + t][bc + 8 * n + g]),
+                     tf32_bits(M[br + 8 * k + t + 4][bc + 8 * n + g]));
     }
 }
-// out(16 x 8 kN at ar.., bc..) = -F B: F (16 x 8 kK) from accumulators.  An accumulator holds
-// columns 2 t and 2 t + 1 where an A operand wants t and t + 4: the depth is walked in
+// c (16 x 8 kN) = F M(rows br .., cols bc ..): F (16 x 8 kK) from accumulators.  An accumulator
+// holds columns 2 t and 2 t + 1 where an A operand wants t and t + 4: the depth is walked in
 // that order on both sides.
 template <int kN, int kK>
-__device__ __forceinline__ void tf32_second(float (*T)[kLd], int orow, int ocol, const float (&f)[kK][4],
-                                            int br, int lane) {
+__device__ __forceinline__ void tf32_second(float (&c)[kN][4], const float (&f)[kK][4], const float (*M)[kLd], int br,
+                                            int bc, int lane) {
     const int g = lane >> 2, t = lane & 3;
 #pragma unroll
     for (int n = 0; n < kN; ++n) {
-        float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        c[n][0] = c[n][1] = c[n][2] = c[n][3] = 0.0f;
 #pragma unroll
         for (int k = 0; k < kK; ++k) {
             const uint32_t a[4] = {tf32_bits(f[k][0]), tf32_bits(f[k][2]), tf32_bits(f[k][1]), tf32_bits(f[k][3])};
-            mma_tf32(c, a, tf32_bits(T[br + 8 * k + 2 * t][ocol + 8 * n + g]),
-                     tf32_bits(T[br + 8 * k + 2 * t + 1][ocol + 8 * n + g]));
+            mma_tf32(c[n], a, tf32_bits(M[br + 8 * k + 2 * t][bc + 8 * n + g]),
+                     tf32_bits(M[br + 8 * k + 2 * t + 1][bc + 8 * n + g]));
         }
-        T[orow + g][ocol + 8 * n + 2 * t] = -c[0];
-        T[orow + g][ocol + 8 * n + 2 * t + 1] = -c[1];
-        T[orow + g + 8][ocol + 8 * n + 2 * t] = -c[2];
-        T[orow + g + 8][ocol + 8 * n + 2 * t + 1] = -c[3];
+    }
+}
+// M(16 x 8 kN at row, col) = -c
+template <int kN>
+__device__ __forceinline__ void put_negative(float (*M)[kLd], int row, int col, const float (&c)[kN][4], int lane) {
+    const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+    for (int n = 0; n < kN; ++n) {
+        *reinterpret_cast<float2*>(&M[row + g][col + 8 * n + 2 * t]) = make_float2(-c[n][0], -c[n][1]);
+        *reinterpret_cast<float2*>(&M[row + g + 8][col + 8 * n + 2 * t]) = make_float2(-c[n][2], -c[n][3]);
     }
 }
 
-__global__ void __launch_bounds__(kPrepThreads) gdr_prep_kernel(GdrChunked P) {
+__global__ void __launch_bounds__(kPrepThreads, 5) gdr_prep_kernel(GdrChunked P) {
     extern __shared__ __align__(128) unsigned char raw[];
     PrepSmem& S = *reinterpret_cast<PrepSmem*>(raw);
     const GdrInputs& I = P.in;
-    const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, g = lane >> 2, t = lane & 3;
+    const int tid = threadIdx.x, lane = tid & 31, g = lane >> 2, t = lane & 3;
     const int chunk = blockIdx.x, hk = blockIdx.y;
+    // rows of this warp; the last ones have four times the work of the first, so the warps of
+    // one scheduler take different ones in different CTAs
+    const int w = ((tid >> 5) + chunk) & 3;
     int n, c;
     if (!find_chunk(I, P.chunks, chunk, n, c)) return;
     const Span span = span_of(I, P.chunks, n);
     const long long tok = span.start + (long long)c * kC;
     const int rows = min(kC, span.len - c * kC);
-    const uint32_t sk = smem_u32(S.k), sq = smem_u32(S.q);
+    const uint32_t sk = smem_u32(S.k), sq = smem_u32(S.q), sp = smem_u32(S.p);
     load_tile(sk, I.k + tok * I.k_stride + hk * kDim, I.k_stride, rows, tid);
     load_tile(sq, I.q + tok * I.q_stride + hk * kDim, I.q_stride, rows, tid);
     cp_async_commit();
+    // gates of two tokens per lane of warp 0, one value head ahead
+    const int share = I.Hv / I.Hk;
+    float g0 = 0.0f, g1 = 0.0f, b0 = 0.0f, b1 = 0.0f;
+    const auto fetch_gates = [&](int h) {
+        if (w != 0) return;
+        const size_t at = (size_t)(tok + 2 * lane) * I.Hv + h;
+        g0 = g1 = b0 = b1 = 0.0f;
+        if (2 * lane < rows) {
+            g0 = load_gate(I.g, I.gate_dtype, at);
+            b0 = load_gate(I.beta, I.gate_dtype, at);
+        }
+        if (2 * lane + 1 < rows) {
+            g1 = load_gate(I.g, I.gate_dtype, at + I.Hv);
+            b1 = load_gate(I.beta, I.gate_dtype, at + I.Hv);
+        }
+    };
+    fetch_gates(hk * share);
     cp_async_wait<0>();
     __syncthreads();
     // rows 16 w ..  of K K^T and Q K^T, columns 0 .. 16 w + 15
@@ -160,21 +196,12 @@ __global__ void __launch_bounds__(kPrepThreads) gdr_prep_kernel(GdrChunked P) {
             mma_bf16(qk[2 * np + 1], aq, b[2], b[3]);
         }
     }
-    const int share = I.Hv / I.Hk;
     for (int h = hk * share; h < (hk + 1) * share; ++h) {
-        __syncthreads();               // Q, and the last head's tiles, have been read
+        __syncthreads();               // K and Q, or the last head's tiles, have been read
         unsigned char* block = P.blocks + ((size_t)chunk * I.Hv + h) * kBlockBytes;
-        if (w == 0) {                  // two tokens per lane
-            const size_t at = (size_t)(tok + 2 * lane) * I.Hv + h;
-            float g0 = 0.0f, g1 = 0.0f, b0 = 0.0f, b1 = 0.0f;
-            if (2 * lane < rows) {
-                g0 = load_gate(I.g, I.gate_dtype, at) * kLog2e;
-                b0 = load_gate(I.beta, I.gate_dtype, at);
-            }
-            if (2 * lane + 1 < rows) {
-                g1 = load_gate(I.g, I.gate_dtype, at + I.Hv) * kLog2e;
-                b1 = load_gate(I.beta, I.gate_dtype, at + I.Hv);
-            }
+        if (w == 0) {
+            g0 *= kLog2e;
+            g1 *= kLog2e;
             // 2^-160 is 0 in fp32 already: lower logs (-inf) only would spoil the differences
             g0 = g0 < -160.0f ? -160.0f : g0;
             g1 = g1 < -160.0f ? -160.0f : g1;
@@ -198,6 +225,7 @@ __global__ void __launch_bounds__(kPrepThreads) gdr_prep_kernel(GdrChunked P) {
             reinterpret_cast<float2*>(gates + kGateEnd)[lane] = make_float2(ex2_approx(last - x0), ex2_approx(last - x));
             reinterpret_cast<float2*>(gates + kGateG)[lane] = make_float2(x0, x);
             if (lane == 0) gates[kGateAll] = ex2_approx(last);
+            if (h + 1 < (hk + 1) * share) fetch_gates(h + 1);
         }
         __syncthreads();
         // A in fp32 and P in fp16
@@ -230,57 +258,77 @@ __global__ void __launch_bounds__(kPrepThreads) gdr_prep_kernel(GdrChunked P) {
                 p[2] = pack_half2(pv[1][0], pv[1][1]);
                 p[3] = pack_half2(pv[1][2], pv[1][3]);
             }
-            stsm(a_addr<128>(sq, 16 * w, 2 * np, lane), p[0], p[1], p[2], p[3]);
+            stsm(a_addr<128>(sp, 16 * w, 2 * np, lane), p[0], p[1], p[2], p[3]);
         }
         __syncwarp();
-        // inverse of this warp's diagonal block, a column per lane
-        if (lane < 16) {
+        // inverse of this warp's diagonal block, a column per lane (both halves of the warp alike)
+        {
+            const int d = 16 * w, col = lane & 15;
             float x[16];
 #pragma unroll
             for (int r = 0; r < 16; ++r) {
-                float s = r == lane ? 1.0f : 0.0f;
+                float even = r == col ? 1.0f : 0.0f, odd = 0.0f;
 #pragma unroll
-                for (int m = 0; m < r; ++m) s = fmaf(-S.a[16 * w + r][16 * w + m], x[m], s);
-                x[r] = s;
-                S.t[16 * w + r][16 * w + lane] = s;
+                for (int m = 0; m < r; m += 4) {
+                    const float4 v = *reinterpret_cast<const float4*>(&S.a[d + r][d + m]);
+                    even = fmaf(-v.x, x[m], even);
+                    if (m + 1 < r) odd = fmaf(-v.y, x[m + 1], odd);
+                    if (m + 2 < r) even = fmaf(-v.z, x[m + 2], even);
+                    if (m + 3 < r) odd = fmaf(-v.w, x[m + 3], odd);
+                }
+                x[r] = even + odd;
+            }
+            __syncwarp();
+            if (lane < 16) {
+#pragma unroll
+                for (int r = 0; r < 16; ++r) S.a[d + r][d + col] = x[r];
             }
         }
         __syncthreads();
         {   // blocks of 16: T21 = -(T22 A21) T11, half of the columns per warp
             const int r0 = 32 * (w >> 1);
-            float f[2][4];
-            tf32_product<2, 2>(f, S.t, r0 + 16, r0 + 16, S.a, r0 + 16, r0, lane);
-            tf32_second<1, 2>(S.t, r0 + 16, r0 + 8 * (w & 1), f, r0, lane);
+            float f[2][4], c16[1][4];
+            tf32_product<2, 2>(f, S.a, r0 + 16, r0 + 16, r0 + 16, r0, lane);
+            tf32_second<1, 2>(c16, f, S.a, r0, r0 + 8 * (w & 1), lane);
+            __syncthreads();           // A21 has been read
+            put_negative<1>(S.a, r0 + 16, r0 + 8 * (w & 1), c16, lane);
             // zeros above the diagonal blocks, which the next products read
             if (w & 1) {
 #pragma unroll
-                for (int i = lane; i < 16 * 16; i += 32) S.t[r0 + (i >> 4)][r0 + 16 + (i & 15)] = 0.0f;
+                for (int i = lane; i < 16 * 16; i += 32) S.a[r0 + (i >> 4)][r0 + 16 + (i & 15)] = 0.0f;
             }
         }
         __syncthreads();
         {   // blocks of 32: 16 rows and 16 columns per warp
             const int r0 = 32 + 16 * (w >> 1);
-            float f[4][4];
-            tf32_product<4, 4>(f, S.t, r0, 32, S.a, 32, 0, lane);
-            tf32_second<2, 4>(S.t, r0, 16 * (w & 1), f, 0, lane);
+            float f[4][4], c32[2][4];
+            tf32_product<4, 4>(f, S.a, r0, 32, 32, 0, lane);
+            tf32_second<2, 4>(c32, f, S.a, 0, 16 * (w & 1), lane);
+            __syncthreads();
+            put_negative<2>(S.a, r0, 16 * (w & 1), c32, lane);
         }
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < kC * 8 / kPrepThreads; ++i) {
             const int unit = tid & 7, row = (tid >> 3) + i * (kPrepThreads / 8);
-            uint4 x = make_uint4(0u, 0u, 0u, 0u);
+            uint4 x = make_uint4(0u, 0u, 0u, 0u), y = x;
             if (8 * unit <= row) {
-                const float4 lo = *reinterpret_cast<const float4*>(&S.t[row][8 * unit]);
-                const float4 hi = *reinterpret_cast<const float4*>(&S.t[row][8 * unit + 4]);
-                const int d = row - 8 * unit;      // columns after the diagonal are not part of T
-                x.x = pack_half2(lo.x, d >= 1 ? lo.y : 0.0f);
-                x.y = pack_half2(d >= 2 ? lo.z : 0.0f, d >= 3 ? lo.w : 0.0f);
-                x.z = pack_half2(d >= 4 ? hi.x : 0.0f, d >= 5 ? hi.y : 0.0f);
-                x.w = pack_half2(d >= 6 ? hi.z : 0.0f, d >= 7 ? hi.w : 0.0f);
+                const float4 lo = *reinterpret_cast<const float4*>(&S.a[row][8 * unit]);
+                const float4 hi = *reinterpret_cast<const float4*>(&S.a[row][8 * unit + 4]);
+                float f[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+                for (int j = 1; j < 8; ++j)      // columns after the diagonal are not part of T
+                    if (8 * unit + j > row) f[j] = 0.0f;
+                const float* b = S.b + 8 * unit;
+                x = make_uint4(pack_half2(f[0] * b[0], f[1] * b[1]), pack_half2(f[2] * b[2], f[3] * b[3]),
+                               pack_half2(f[4] * b[4], f[5] * b[5]), pack_half2(f[6] * b[6], f[7] * b[7]));
+                y = make_uint4(pack_half2(f[0], f[1]), pack_half2(f[2], f[3]), pack_half2(f[4], f[5]), pack_half2(f[6], f[7]));
             }
             const int at = row * 128 + ((unit ^ (row & 7)) << 4);
             *reinterpret_cast<uint4*>(block + at) = x;
-            *reinterpret_cast<uint4*>(block + kTileBytes + at) = *reinterpret_cast<const uint4*>(S.q + at);
+            if (P.ts)
+                *reinterpret_cast<uint4*>(P.ts + ((size_t)chunk * I.Hv + h) * kTileBytes + at) = y;
+            *reinterpret_cast<uint4*>(block + kTileBytes + at) = *reinterpret_cast<const uint4*>(S.p + at);
         }
     }
 }

@@ -16,6 +16,11 @@ int cuda_fail(int status, cudaError_t e);
 // compute capability 10.3 GPU.  Set up once per device.
 int device_setup(int* dev_out, int** err_out, int* sms_out = nullptr);
 
+// Tensor map of `rows` rows of `inner` 16-bit elements, `pitch` elements apart, for boxes of 64
+// elements x `box_rows` rows in the 128-byte swizzle.
+cudaError_t encode_rows_map(CUtensorMap* map, const void* base, long long inner, long long rows,
+                            long long pitch, int box_rows);
+
 // Records the launches between its construction and its destruction, with their device
 // time, under a kernel id (kda_profile_*); nothing while recording is off.
 class LaunchTimer {

@@ -437,7 +437,7 @@ int kda_gdr_fwd(const void* q, const void* k, const void* v, const void* g, cons
  * sums, whatever the gates' type: the incoming gradients are scaled per (sequence, key head)
  * by the power of two that brings the largest to 16 .. 32, so gradients of any size keep it;
  * q, k, v and the states have to stay below 65,504 as in kda_gdr_fwd.  Deterministic.
- * Scratch: kda_gdr_bwd_workspace_bytes() from the stream-ordered allocator (about 1.8 KB per
+ * Scratch: kda_gdr_bwd_workspace_bytes() from the stream-ordered allocator (about 1.9 KB per
  * token and value head).
  */
 int kda_gdr_bwd(const void* q, const void* k, const void* v, const void* g, const void* beta,

@@ -182,5 +182,5 @@ def test_bwd_workspace_bytes():
     import gated_delta_rule_39_gb300 as kda
     assert kda.kda_gdr_bwd_workspace_bytes(1, 0, 1, 1) < 4096
     per = kda.kda_gdr_bwd_workspace_bytes(1, 64000, 1, 2) / 128000
-    assert 1700 < per < 1900
+    assert 1850 < per < 2050
     assert kda.kda_gdr_bwd_workspace_bytes(1, 64, 1, 1, 7, True) >= 8 * 17680
