@@ -24,6 +24,13 @@ namespace kda {
 namespace {
 
 constexpr int kNormThreads = 256;
+// Heads that a group of the forward pass holds at a time: as many as 128 registers have room for.
+__host__ __device__ constexpr int rows_at_once(int vec) { return vec > 1 ? 2 : 1; }
+constexpr int kManyHeads = 8;             // of a token, at most, for a group that reads its angles once
+constexpr int kFwdPerSm = 2;              // blocks of the forward pass
+// Blocks of the backward pass: three where 80 registers hold a lane's part (16-byte bf16
+// accesses, no angles, weights or their gradients), else two.
+__host__ __device__ constexpr int bwd_per_sm(int vec, bool more) { return vec == 8 && !more ? 3 : 2; }
 constexpr int kNormMaxDim = 512;
 
 struct NormSide {             // the queries' part of a call, or the keys'
@@ -32,8 +39,10 @@ struct NormSide {             // the queries' part of a call, or the keys'
     void* y;                  // z, or dL/dx (contiguous rows)
     const float* w;           // [D] or nullptr
     float* dw_part;           // backward: [blocks][D] partial sums, or nullptr
+    float* dw;                // and their sums [D]
     long long stride;         // elements from one token of x to the next
     int heads;
+    int blocks;               // backward: blocks that walk this side's rows
 };
 
 struct NormProblem {
@@ -115,15 +124,27 @@ __device__ __forceinline__ void slot_channels(int slot, int half, int inter, int
         u1 = 2 * first + VEC;
     }
 }
-// A slot's channels in a row: pair i is (a[i], b[i]) when the slot is rotated.
+// A slot's channels as they are in memory: two units.
+template <typename T, int VEC>
+struct __align__(sizeof(T) * VEC) Unit {
+    T v[VEC];
+};
+template <typename T, int VEC>
+struct Raw {
+    Unit<T, VEC> e0, e1;
+};
 template <int VEC, typename T>
-__device__ __forceinline__ void load_slot(const T* row, int slot, int half, int inter,
-                                          float (&a)[VEC], float (&b)[VEC]) {
+__device__ __forceinline__ Raw<T, VEC> fetch_slot(const T* row, int slot, int half, int inter) {
     int u0, u1;
     slot_channels<VEC>(slot, half, inter, u0, u1);
+    return {*reinterpret_cast<const Unit<T, VEC>*>(row + u0), *reinterpret_cast<const Unit<T, VEC>*>(row + u1)};
+}
+// A slot's channels: pair i is (a[i], b[i]) when the slot is rotated.
+template <int VEC, typename T>
+__device__ __forceinline__ void spread(const Raw<T, VEC>& r, int inter, float (&a)[VEC], float (&b)[VEC]) {
     float e0[VEC], e1[VEC];
-    load_vec<VEC>(row + u0, e0);
-    load_vec<VEC>(row + u1, e1);
+    load_vec<VEC>(r.e0.v, e0);
+    load_vec<VEC>(r.e1.v, e1);
 #pragma unroll
     for (int i = 0; i < VEC; ++i) {
         if (VEC > 1 && inter) {
@@ -134,6 +155,10 @@ __device__ __forceinline__ void load_slot(const T* row, int slot, int half, int 
             b[i] = e1[i];
         }
     }
+}
+template <int VEC, typename T>
+__device__ __forceinline__ void load_slot(const T* row, int slot, int half, int inter, float (&a)[VEC], float (&b)[VEC]) {
+    spread<VEC>(fetch_slot<VEC>(row, slot, half, inter), inter, a, b);
 }
 template <int VEC, typename T>
 __device__ __forceinline__ void store_slot(T* row, int slot, int half, int inter,
@@ -153,11 +178,6 @@ __device__ __forceinline__ void store_slot(T* row, int slot, int half, int inter
     }
     store_vec<VEC>(row + u0, e0);
     store_vec<VEC>(row + u1, e1);
-}
-
-__device__ __forceinline__ float group_sum(float x, int lanes) {
-    for (int o = lanes >> 1; o > 0; o >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, o);
-    return x;
 }
 
 // The angles of a slot at a token (1, 0 where it is not rotated); false: bad position.
@@ -180,172 +200,266 @@ __device__ __forceinline__ bool load_angles(const NormProblem& P, int t, int slo
     return true;
 }
 
-// One group of P.lanes lanes per row (token, head); NS slots per lane.  The rows of the
-// queries come first, then the keys'.
+// An item is up to `hb` heads of a token, the work of one group of P.lanes lanes with NS slots per
+// lane, so that angles and weights, in fp32 twice a bf16 row's bytes each, are read once for all
+// of them.  The queries' items come first, then the keys'; groups walk them with a stride,
+// R heads at a time with the next ones' rows on their way.
+__host__ __device__ inline unsigned head_blocks(int heads, int hb) { return ((unsigned)heads + hb - 1) / hb; }
+
 template <typename T, int VEC, int NS>
-__global__ void __launch_bounds__(kNormThreads) qk_norm_kernel(NormProblem P) {
-    const int per_warp = 32 / P.lanes;
-    const int lane = threadIdx.x & 31, li = lane % P.lanes;
-    const long long warp = (long long)blockIdx.x * (kNormThreads / 32) + (threadIdx.x >> 5);
-    long long row = warp * per_warp + lane / P.lanes;
-    const long long nq = (long long)P.T * P.side[0].heads;
-    const long long total = nq + (long long)P.T * P.side[1].heads;
-    const bool there = row < total;
-    if (!there) row = total - 1;           // keeps the lane in the butterflies
-    const int w = row >= nq;
-    const NormSide& S = P.side[w];
-    if (w) row -= nq;
-    const int t = (int)(row / S.heads), h = (int)(row % S.heads);
-    const T* x = static_cast<const T*>(S.x) + t * S.stride + (long long)h * P.D;
-    const int slots = P.D / (2 * VEC);
-    float a[NS][VEC], b[NS][VEC], sum = 0.0f;
+__global__ void __launch_bounds__(kNormThreads, kFwdPerSm) qk_norm_kernel(NormProblem P, int hb) {
+    constexpr int R = rows_at_once(VEC);
+    const unsigned per_warp = 32 / P.lanes;
+    const int lane = threadIdx.x & 31, li = lane % P.lanes, slots = P.D / (2 * VEC);
+    const unsigned nq = P.T * head_blocks(P.side[0].heads, hb), total = nq + P.T * head_blocks(P.side[1].heads, hb);
+    const unsigned stride = gridDim.x * (kNormThreads / 32) * per_warp;
+    struct Place {
+        int w, t, h, left;                 // side, token, first head, heads
+    };
+    const auto place = [&](unsigned item) {
+        if (item >= total) return Place{0, 0, 0, 0};
+        const int w = item >= nq;
+        if (w) item -= nq;
+        const int heads = P.side[w].heads;
+        const unsigned blocks = head_blocks(heads, hb);
+        const int h = (int)(item % blocks) * hb;
+        return Place{w, (int)(item / blocks), h, min(hb, heads - h)};
+    };
+    Raw<T, VEC> raw[R][NS] = {};
+    const auto fetch = [&](const Place& p, int j) {
+        const NormSide& S = P.side[p.w];
+        const T* x = static_cast<const T*>(S.x) + p.t * S.stride + (long long)(p.h + j) * P.D;
 #pragma unroll
-    for (int j = 0; j < NS; ++j) {
-        const int slot = li + j * P.lanes;
-        if (slot < slots) {
-            load_slot<VEC>(x, slot, P.half, P.inter, a[j], b[j]);
+        for (int r = 0; r < R; ++r)
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) sum += a[j][i] * a[j][i] + b[j][i] * b[j][i];
+            for (int m = 0; m < NS; ++m)
+                if (j + r < p.left && li + m * P.lanes < slots)
+                    raw[r][m] = fetch_slot<VEC>(x + r * P.D, li + m * P.lanes, P.half, P.inter);
+    };
+    unsigned first = (blockIdx.x * (kNormThreads / 32) + (threadIdx.x >> 5)) * per_warp;
+    Place now = place(first + lane / P.lanes);
+    fetch(now, 0);
+    float wa[NS][VEC], wb[NS][VEC];
+    int have = -1;                         // the side whose weights these are
+    // whole warps walk together: a warp's first item decides
+    while (first < total) {
+        const Place next = place(first + stride + lane / P.lanes);
+        const NormSide& S = P.side[now.w];
+        float cs[NS][VEC], sn[NS][VEC];
+        bool good = now.left > 0;
+#pragma unroll
+        for (int m = 0; m < NS; ++m) {
+            const int slot = li + m * P.lanes;
+            if (now.left && !load_angles<VEC>(P, now.t, slot, cs[m], sn[m])) {
+                set_error(P.err, KDA_ERR_BAD_INDEX);
+                good = false;
+            }
+            if (have != now.w) {
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) wa[m][i] = wb[m][i] = 1.0f;
+                if (S.w && slot < slots) load_slot<VEC>(S.w, slot, P.half, P.inter, wa[m], wb[m]);
+            }
         }
-    }
-    const float r = 1.0f / sqrtf(P.c * group_sum(sum, P.lanes) + P.eps);
-    T* z = static_cast<T*>(S.y) + row * P.D;
+        have = now.w;
+        T* z = static_cast<T*>(S.y) + ((long long)now.t * S.heads + now.h) * P.D;
+#pragma unroll 1
+        for (int j = 0; j < hb; j += R) {
+            float a[R][NS][VEC], b[R][NS][VEC], sum[R];
 #pragma unroll
-    for (int j = 0; j < NS; ++j) {
-        const int slot = li + j * P.lanes;
-        if (slot >= slots || !there) continue;
-        float cs[VEC], sn[VEC], wa[VEC], wb[VEC];
-        if (!load_angles<VEC>(P, t, slot, cs, sn)) {
-            set_error(P.err, KDA_ERR_BAD_INDEX);
-            continue;
-        }
-        if (S.w) load_slot<VEC>(S.w, slot, P.half, P.inter, wa, wb);
+            for (int r = 0; r < R; ++r) {
+                sum[r] = 0.0f;
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-            const float ya = a[j][i] * r * (S.w ? wa[i] : 1.0f), yb = b[j][i] * r * (S.w ? wb[i] : 1.0f);
-            a[j][i] = ya * cs[i] - yb * sn[i];
-            b[j][i] = yb * cs[i] + ya * sn[i];
+                for (int m = 0; m < NS; ++m) {     // slots past the row are zeros
+                    spread<VEC>(raw[r][m], P.inter, a[r][m], b[r][m]);
+#pragma unroll
+                    for (int i = 0; i < VEC; ++i) sum[r] += a[r][m][i] * a[r][m][i] + b[r][m][i] * b[r][m][i];
+                }
+            }
+            if (j + R < hb) fetch(now, j + R);
+            else fetch(next, 0);
+            for (int o = P.lanes >> 1; o > 0; o >>= 1)
+#pragma unroll
+                for (int r = 0; r < R; ++r) sum[r] += __shfl_xor_sync(0xFFFFFFFFu, sum[r], o);
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                if (!good || j + r >= now.left) continue;
+                const float k = 1.0f / sqrtf(P.c * sum[r] + P.eps);
+#pragma unroll
+                for (int m = 0; m < NS; ++m) {
+                    const int slot = li + m * P.lanes;
+                    if (slot >= slots) continue;
+#pragma unroll
+                    for (int i = 0; i < VEC; ++i) {
+                        const float ya = a[r][m][i] * k * wa[m][i], yb = b[r][m][i] * k * wb[m][i];
+                        a[r][m][i] = ya * cs[m][i] - yb * sn[m][i];
+                        b[r][m][i] = yb * cs[m][i] + ya * sn[m][i];
+                    }
+                    store_slot<VEC>(z + (j + r) * P.D, slot, P.half, P.inter, a[r][m], b[r][m]);
+                }
+            }
         }
-        store_slot<VEC>(z, slot, P.half, P.inter, a[j], b[j]);
+        now = next;
+        first += stride;
     }
 }
 
-// Backward: blockIdx.y picks the queries or the keys, whose rows the grid's groups walk
-// with a stride; each lane sums its channels of dw over its rows, and the block writes one
-// partial row of D sums (in a fixed order: results do not depend on scheduling).
-template <typename T, int VEC, int NS>
-__global__ void __launch_bounds__(kNormThreads) qk_norm_bwd_kernel(NormProblem P) {
-    __shared__ __align__(16) float part[kNormThreads / 32][kNormMaxDim];
-    const NormSide& S = P.side[blockIdx.y];
+// Backward: the first blocks take the queries, the others the keys; a side's groups walk its items
+// with a stride, a head at a time with the next head's row on its way.  Each lane sums its
+// channels of dw over its rows, and the block writes one partial row of D sums (in a fixed order:
+// results do not depend on scheduling).
+template <typename T, int VEC, int NS, bool kRot, bool kW>
+__global__ void __launch_bounds__(kNormThreads, bwd_per_sm(VEC, kRot || kW)) qk_norm_bwd_kernel(NormProblem P, int hb) {
+    __shared__ __align__(16) float part[kW ? kNormThreads / 32 : 1][kNormMaxDim];
+    const int side = blockIdx.x >= P.side[0].blocks, block = blockIdx.x - (side ? P.side[0].blocks : 0);
+    const NormSide& S = P.side[side];
     const int per_warp = 32 / P.lanes;
     const int lane = threadIdx.x & 31, li = lane % P.lanes, wid = threadIdx.x >> 5;
-    const long long groups = (long long)gridDim.x * (kNormThreads / 32) * per_warp;
-    const long long rows = (long long)P.T * S.heads;
+    const unsigned hblocks = head_blocks(S.heads, hb), items = P.T * hblocks;
+    const unsigned stride = S.blocks * (kNormThreads / 32) * per_warp;
     const int slots = P.D / (2 * VEC);
     float wa[NS][VEC], wb[NS][VEC], ga[NS][VEC], gb[NS][VEC];
 #pragma unroll
-    for (int j = 0; j < NS; ++j) {
+    for (int m = 0; m < NS; ++m) {
 #pragma unroll
         for (int i = 0; i < VEC; ++i) {
-            wa[j][i] = wb[j][i] = 1.0f;
-            ga[j][i] = gb[j][i] = 0.0f;
+            wa[m][i] = wb[m][i] = 1.0f;
+            ga[m][i] = gb[m][i] = 0.0f;
         }
-        const int slot = li + j * P.lanes;
-        if (S.w && slot < slots) load_slot<VEC>(S.w, slot, P.half, P.inter, wa[j], wb[j]);
+        const int slot = li + m * P.lanes;
+        if (kW && S.w && slot < slots) load_slot<VEC>(S.w, slot, P.half, P.inter, wa[m], wb[m]);
     }
-    // whole warps leave the loop together: a warp's first row decides
-    for (long long first = ((long long)blockIdx.x * (kNormThreads / 32) + wid) * per_warp; first < rows;
-         first += groups) {
-        long long row = first + lane / P.lanes;
-        const bool there = row < rows;
-        if (!there) row = rows - 1;
-        const int t = (int)(row / S.heads), h = (int)(row % S.heads);
+    Raw<T, VEC> rx[NS] = {}, rz[NS] = {};
+    const auto fetch = [&](int t, int h) {
         const T* x = static_cast<const T*>(S.x) + t * S.stride + (long long)h * P.D;
-        const T* dz = static_cast<const T*>(S.dz) + row * P.D;
-        float a[NS][VEC], b[NS][VEC], da[NS][VEC], db[NS][VEC], sum = 0.0f, dot = 0.0f;
+        const T* dz = static_cast<const T*>(S.dz) + ((long long)t * S.heads + h) * P.D;
+#pragma unroll
+        for (int m = 0; m < NS; ++m)
+            if (li + m * P.lanes < slots) {
+                rx[m] = fetch_slot<VEC>(x, li + m * P.lanes, P.half, P.inter);
+                rz[m] = fetch_slot<VEC>(dz, li + m * P.lanes, P.half, P.inter);
+            }
+    };
+    // whole warps leave the loop together: a warp's first item decides, and the lanes of items past
+    // the end repeat the last one without writing
+    unsigned first = (block * (kNormThreads / 32) + wid) * per_warp;
+    unsigned item = min(first + lane / P.lanes, items - 1);
+    int t = (int)(item / hblocks), h = (int)(item % hblocks) * hb;
+    if (first < items) fetch(t, h);
+    while (first < items) {
+        const bool there = first + lane / P.lanes < items;
+        float cs[NS][VEC], sn[NS][VEC];
         bool good = there;
+        if (kRot) {
 #pragma unroll
-        for (int j = 0; j < NS; ++j) {
-            const int slot = li + j * P.lanes;
-            if (slot >= slots) continue;
-            load_slot<VEC>(x, slot, P.half, P.inter, a[j], b[j]);
-            load_slot<VEC>(dz, slot, P.half, P.inter, da[j], db[j]);
-            float cs[VEC], sn[VEC];
-            if (!load_angles<VEC>(P, t, slot, cs, sn)) {
-                if (there) set_error(P.err, KDA_ERR_BAD_INDEX);
-                good = false;
+            for (int m = 0; m < NS; ++m)
+                if (!load_angles<VEC>(P, t, li + m * P.lanes, cs[m], sn[m])) {
+                    if (there) set_error(P.err, KDA_ERR_BAD_INDEX);
+                    good = false;
+                }
+        }
+        // a warp's groups may have fewer heads left than others: all take hb turns
+        const unsigned next = first + stride;
+        const int t0 = t, h0 = h;
+        if (next < items) {
+            item = min(next + lane / P.lanes, items - 1);
+            t = (int)(item / hblocks);
+            h = (int)(item % hblocks) * hb;
+        }
+#pragma unroll 1
+        for (int j = 0; j < hb; ++j) {
+            const bool mine = good && h0 + j < S.heads;
+            float a[NS][VEC], b[NS][VEC], da[NS][VEC], db[NS][VEC], sum = 0.0f, dot = 0.0f;
+#pragma unroll
+            for (int m = 0; m < NS; ++m) {
+                spread<VEC>(rx[m], P.inter, a[m], b[m]);
+                spread<VEC>(rz[m], P.inter, da[m], db[m]);
             }
+            if (j + 1 < hb) fetch(t0, min(h0 + j + 1, S.heads - 1));
+            else if (next < items) fetch(t, h);
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-                const float ya = da[j][i] * cs[i] + db[j][i] * sn[i];
-                db[j][i] = db[j][i] * cs[i] - da[j][i] * sn[i];
-                da[j][i] = ya;
-                sum += a[j][i] * a[j][i] + b[j][i] * b[j][i];
-                dot += a[j][i] * (wa[j][i] * da[j][i]) + b[j][i] * (wb[j][i] * db[j][i]);
+            for (int m = 0; m < NS; ++m) {
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) {
+                    if (kRot) {
+                        const float ya = da[m][i] * cs[m][i] + db[m][i] * sn[m][i];
+                        db[m][i] = db[m][i] * cs[m][i] - da[m][i] * sn[m][i];
+                        da[m][i] = ya;
+                    }
+                    sum += a[m][i] * a[m][i] + b[m][i] * b[m][i];
+                    dot += a[m][i] * (wa[m][i] * da[m][i]) + b[m][i] * (wb[m][i] * db[m][i]);
+                }
+            }
+            for (int o = P.lanes >> 1; o > 0; o >>= 1) {
+                sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+                dot += __shfl_xor_sync(0xFFFFFFFFu, dot, o);
+            }
+            if (!mine) continue;
+            const float r = 1.0f / sqrtf(P.c * sum + P.eps), k = P.c * r * r * dot;
+            T* dx = static_cast<T*>(S.y) + ((long long)t0 * S.heads + h0 + j) * P.D;
+#pragma unroll
+            for (int m = 0; m < NS; ++m) {
+                const int slot = li + m * P.lanes;
+                if (slot >= slots) continue;
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) {
+                    if (kW) {
+                        ga[m][i] += da[m][i] * (a[m][i] * r);
+                        gb[m][i] += db[m][i] * (b[m][i] * r);
+                    }
+                    a[m][i] = r * (wa[m][i] * da[m][i] - a[m][i] * k);
+                    b[m][i] = r * (wb[m][i] * db[m][i] - b[m][i] * k);
+                }
+                store_slot<VEC>(dx, slot, P.half, P.inter, a[m], b[m]);
             }
         }
-        const float r = 1.0f / sqrtf(P.c * group_sum(sum, P.lanes) + P.eps);
-        const float m = P.c * r * r * group_sum(dot, P.lanes);
-        if (!good) continue;
-        T* dx = static_cast<T*>(S.y) + row * P.D;
-#pragma unroll
-        for (int j = 0; j < NS; ++j) {
-            const int slot = li + j * P.lanes;
-            if (slot >= slots) continue;
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-                ga[j][i] += da[j][i] * (a[j][i] * r);
-                gb[j][i] += db[j][i] * (b[j][i] * r);
-                a[j][i] = r * (wa[j][i] * da[j][i] - a[j][i] * m);
-                b[j][i] = r * (wb[j][i] * db[j][i] - b[j][i] * m);
-            }
-            store_slot<VEC>(dx, slot, P.half, P.inter, a[j], b[j]);
-        }
+        first = next;
     }
-    if (!S.dw_part) return;
-    // groups of a warp, then the block's warps
+    if constexpr (kW) {
+        if (!S.dw_part) return;
+        // groups of a warp, then the block's warps
 #pragma unroll
-    for (int j = 0; j < NS; ++j)
+        for (int m = 0; m < NS; ++m)
 #pragma unroll
-        for (int i = 0; i < VEC; ++i)
-            for (int o = P.lanes; o < 32; o <<= 1) {
-                ga[j][i] += __shfl_xor_sync(0xFFFFFFFFu, ga[j][i], o);
-                gb[j][i] += __shfl_xor_sync(0xFFFFFFFFu, gb[j][i], o);
+            for (int i = 0; i < VEC; ++i)
+                for (int o = P.lanes; o < 32; o <<= 1) {
+                    ga[m][i] += __shfl_xor_sync(0xFFFFFFFFu, ga[m][i], o);
+                    gb[m][i] += __shfl_xor_sync(0xFFFFFFFFu, gb[m][i], o);
+                }
+        if (lane < P.lanes) {
+#pragma unroll
+            for (int m = 0; m < NS; ++m) {
+                const int slot = li + m * P.lanes;
+                if (slot < slots) store_slot<VEC>(part[wid], slot, P.half, P.inter, ga[m], gb[m]);
             }
-    if (lane < P.lanes) {
-#pragma unroll
-        for (int j = 0; j < NS; ++j) {
-            const int slot = li + j * P.lanes;
-            if (slot < slots) store_slot<VEC>(part[wid], slot, P.half, P.inter, ga[j], gb[j]);
         }
-    }
-    __syncthreads();
-    for (int ch = threadIdx.x; ch < P.D; ch += kNormThreads) {
-        float s = 0.0f;
+        __syncthreads();
+        for (int ch = threadIdx.x; ch < P.D; ch += kNormThreads) {
+            float s = 0.0f;
 #pragma unroll
-        for (int i = 0; i < kNormThreads / 32; ++i) s += part[i][ch];
-        S.dw_part[(size_t)blockIdx.x * P.D + ch] = s;
+            for (int i = 0; i < kNormThreads / 32; ++i) s += part[i][ch];
+            S.dw_part[(size_t)block * P.D + ch] = s;
+        }
     }
 }
 
-// dw[ch] = sum over blocks of part[block][ch]; one block of 8 warps per 32 channels
-__global__ void __launch_bounds__(256) qk_norm_dw_kernel(const float* part0, const float* part1, float* dw0,
-                                                         float* dw1, int blocks, int D) {
-    __shared__ float s[8][33];
-    const float* part = blockIdx.y ? part1 : part0;
-    float* dw = blockIdx.y ? dw1 : dw0;
-    if (!dw) return;
+// dw[ch] = sum over blocks of part[block][ch]; one block of 32 warps per side and 32 channels
+constexpr int kDwThreads = 1024;
+__global__ void __launch_bounds__(kDwThreads) qk_norm_dw_kernel(NormProblem P) {
+    __shared__ float s[kDwThreads / 32][33];
+    const NormSide& S = P.side[blockIdx.y];
+    if (!S.dw_part) return;
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, ch = blockIdx.x * 32 + lane;
     float sum = 0.0f;
-    if (ch < D)
-        for (int i = w; i < blocks; i += 8) sum += part[(size_t)i * D + ch];
+    if (ch < P.D)
+#pragma unroll 8
+        for (int i = w; i < S.blocks; i += kDwThreads / 32) sum += S.dw_part[(size_t)i * P.D + ch];
     s[w][lane] = sum;
     __syncthreads();
-    if (w == 0 && ch < D) {
+    if (w == 0 && ch < P.D) {
         sum = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) sum += s[i][lane];
-        dw[ch] = sum;
+        for (int i = 0; i < kDwThreads / 32; ++i) sum += s[i][lane];
+        S.dw[ch] = sum;
     }
 }
 
@@ -381,28 +495,73 @@ int group_lanes(int slots) {
     return lanes;
 }
 
+long long blocks_for(long long items, int lanes) {
+    const long long per_block = kNormThreads / lanes;
+    return (items + per_block - 1) / per_block;
+}
+
+// Heads of an item: as many as share angles and weights well, but a group keeps four items at
+// least, so that few rows are spread over all groups and the walk ends evenly.
+int item_heads(long long rows, int least, int lanes, int blocks) {
+    const long long groups = (long long)blocks * (kNormThreads / lanes);
+    int hb = least;
+    while (hb < kManyHeads && rows >= 4 * groups * 2 * hb) hb *= 2;
+    return hb;
+}
+
 struct LaunchFwd {
     NormProblem P;
+    int sms;
     cudaStream_t s;
     template <typename T, int VEC, int NS>
     cudaError_t operator()(int slots) {
         P.lanes = group_lanes(slots);
-        const long long rows = (long long)P.T * (P.side[0].heads + P.side[1].heads);
-        const long long per_block = (long long)kNormThreads / P.lanes;
-        qk_norm_kernel<T, VEC, NS><<<(unsigned)((rows + per_block - 1) / per_block), kNormThreads, 0, s>>>(P);
+        const int room = kFwdPerSm * sms;
+        const int hb = item_heads((long long)P.T * (P.side[0].heads + P.side[1].heads), rows_at_once(VEC), P.lanes, room);
+        const long long items = (long long)P.T * (head_blocks(P.side[0].heads, hb) + head_blocks(P.side[1].heads, hb));
+        qk_norm_kernel<T, VEC, NS><<<(unsigned)std::min<long long>(room, blocks_for(items, P.lanes)), kNormThreads, 0, s>>>(P, hb);
         return cudaGetLastError();
     }
 };
 struct LaunchBwd {
     NormProblem P;
-    int blocks;
+    int sms;
     cudaStream_t s;
+    // blocks between the sides by their rows, and no more than there are items for
+    template <typename T, int VEC, int NS, bool kRot, bool kW>
+    cudaError_t run() {
+        const int heads = P.side[0].heads + P.side[1].heads, room = bwd_per_sm(VEC, kRot || kW) * sms;
+        const int hb = item_heads((long long)P.T * heads, 1, P.lanes, room);
+        for (NormSide& S : P.side)
+            S.blocks = S.heads ? (int)std::max<long long>(1, std::min<long long>((long long)room * S.heads / heads,
+                                                                                 blocks_for((long long)P.T * head_blocks(S.heads, hb), P.lanes)))
+                               : 0;
+        const size_t parts = (size_t)P.side[0].blocks + P.side[1].blocks;
+        float* part = nullptr;
+        if (kW) {
+            const cudaError_t e = cudaMallocAsync(reinterpret_cast<void**>(&part), parts * P.D * 4, s);
+            if (e != cudaSuccess) return e;
+            P.side[0].dw_part = P.side[0].w ? part : nullptr;
+            P.side[1].dw_part = P.side[1].w ? part + (size_t)P.side[0].blocks * P.D : nullptr;
+        }
+        cudaError_t e = timed_launch(KDA_KERNEL_QK_NORM_BWD, s, [&] {
+            qk_norm_bwd_kernel<T, VEC, NS, kRot, kW><<<(unsigned)parts, kNormThreads, 0, s>>>(P, hb);
+            return cudaGetLastError();
+        });
+        if (kW && e == cudaSuccess)
+            e = timed_launch(KDA_KERNEL_QK_NORM_DW, s, [&] {
+                qk_norm_dw_kernel<<<dim3((P.D + 31) / 32, 2), kDwThreads, 0, s>>>(P);
+                return cudaGetLastError();
+            });
+        if (kW) cudaFreeAsync(part, s);
+        return e;
+    }
     template <typename T, int VEC, int NS>
     cudaError_t operator()(int slots) {
         P.lanes = group_lanes(slots);
-        const dim3 grid(blocks, P.side[1].heads ? 2 : 1);
-        qk_norm_bwd_kernel<T, VEC, NS><<<grid, kNormThreads, 0, s>>>(P);
-        return cudaGetLastError();
+        const bool w = P.side[0].w || P.side[1].w;
+        if (P.cos) return w ? run<T, VEC, NS, true, true>() : run<T, VEC, NS, true, false>();
+        return w ? run<T, VEC, NS, false, true>() : run<T, VEC, NS, false, false>();
     }
 };
 
@@ -504,7 +663,7 @@ int kda_qk_norm(const void* q, const void* k, void* q_out, void* k_out, int dtyp
     if (T == 0) return KDA_OK;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     LaunchFwd L{problem(q, k, norm, eps, q_weight, k_weight, cos, sin, positions, table_rows, rotary_dim,
-                        interleaved, T, Hq, Hk, D, q_stride, k_stride, err), s};
+                        interleaved, T, Hq, Hk, D, q_stride, k_stride, err), sms, s};
     L.P.side[0].y = q_out;
     L.P.side[1].y = k_out;
     const cudaError_t e = timed_launch(KDA_KERNEL_QK_NORM, s,
@@ -555,30 +714,16 @@ int kda_qk_norm_bwd(const void* q, const void* k, const void* dq_out, const void
         if (e == cudaSuccess && dk_weight) e = cudaMemsetAsync(dk_weight, 0, (size_t)D * 4, s);
         return e == cudaSuccess ? KDA_OK : cuda_fail(KDA_ERR_CUDA, e);
     }
-    const long long per_block = kNormThreads / 16;   // rows of a block's first pass, or more
-    const int blocks = (int)std::min<long long>(4LL * sms, ((long long)T * std::max(Hq, Hk) + per_block - 1) / per_block);
     LaunchBwd L{problem(q, k, norm, eps, q_weight, k_weight, cos, sin, positions, table_rows, rotary_dim,
-                        interleaved, T, Hq, Hk, D, q_stride, k_stride, err), blocks, s};
+                        interleaved, T, Hq, Hk, D, q_stride, k_stride, err), sms, s};
     L.P.side[0].dz = dq_out;
     L.P.side[1].dz = dk_out;
     L.P.side[0].y = dq;
     L.P.side[1].y = dk;
-    float* part = nullptr;
-    if (dq_weight || dk_weight) {
-        const cudaError_t ea = cudaMallocAsync(reinterpret_cast<void**>(&part), (size_t)2 * blocks * D * 4, s);
-        if (ea != cudaSuccess) return cuda_fail(KDA_ERR_ALLOC, ea);
-        if (dq_weight) L.P.side[0].dw_part = part;
-        if (dk_weight) L.P.side[1].dw_part = part + (size_t)blocks * D;
-    }
-    e = timed_launch(KDA_KERNEL_QK_NORM_BWD, s,
-                     [&] { return with_width(L.P, dtype, wide_ok(L.P, dtype), L); });
-    if (part && e == cudaSuccess)
-        e = timed_launch(KDA_KERNEL_QK_NORM_DW, s, [&] {
-            qk_norm_dw_kernel<<<dim3((D + 31) / 32, 2), 256, 0, s>>>(part, part + (size_t)blocks * D,
-                                                                     dq_weight, dk_weight, blocks, D);
-            return cudaGetLastError();
-        });
-    if (part) cudaFreeAsync(part, s);
+    L.P.side[0].dw = dq_weight;
+    L.P.side[1].dw = dk_weight;
+    e = with_width(L.P, dtype, wide_ok(L.P, dtype), L);
+    if (e == cudaErrorMemoryAllocation) return cuda_fail(KDA_ERR_ALLOC, e);
     if (e != cudaSuccess) return cuda_fail(KDA_ERR_LAUNCH, e);
     return KDA_OK;
 }

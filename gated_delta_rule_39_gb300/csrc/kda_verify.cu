@@ -12,14 +12,14 @@
 // those bytes, or for few sequences by latency.  The division is IEEE's and rest is one
 // subtraction, so the scores, and the winner, do not depend on how the row is split; ties go to
 // the lowest index.
-#include <cmath>
-
 #include "kda_host.cuh"
 
 namespace kda {
 namespace {
 
-constexpr int kVerThreads = 1024;
+constexpr int kVerThreads = 512;
+constexpr int kMaxSplit = 16;             // CTAs (a cluster) for a sequence's row
+constexpr int kMinSlice = 2048;           // elements of a row that a CTA is started for, at least
 
 struct VerifyProblem {
     const void* target;       // [N][D + 1][V]
@@ -37,6 +37,11 @@ struct VerifyProblem {
 __device__ __forceinline__ float prob(const __nv_bfloat16* p, size_t i) { return __bfloat162float(p[i]); }
 __device__ __forceinline__ float prob(const float* p, size_t i) { return p[i]; }
 
+template <typename T, int VEC>
+struct __align__(sizeof(T) * VEC) Unit {
+    T v[VEC];
+};
+
 // Larger score first, then lower index; 0 where the score is not positive (or not a
 // number).  A positive float's bits rise with its value.
 __device__ __forceinline__ unsigned long long race_key(float rest, float noise, int v) {
@@ -50,76 +55,167 @@ __device__ __forceinline__ unsigned long long max_key(unsigned long long a, unsi
     return a > b ? a : b;
 }
 
-// Drafts kept of sequence n, by one warp; -1: a count or a token out of range.
+// Drafts kept of sequence n, by a warp; -1: a count or a token out of range.
 template <typename T>
 __device__ int drafts_kept(const VerifyProblem& P, int n, int lane, int& count) {
     count = P.count ? P.count[n] : P.D;
-    if (count < 0 || count > P.D) return -1;
-    for (int first = 0; first < count; first += 32) {
+    for (int first = 0; first < P.D; first += 32) {
         const int i = first + lane;
         bool keep = true, bad = false;
-        if (i < count) {
+        if (i < P.D) {                         // the loads need not wait for the count
             const size_t at = (size_t)n * P.D + i;
             const int x = P.tokens[at];
-            bad = x < 0 || x >= P.V;
-            if (!bad) {
+            const float u = P.uniform[at];
+            const bool in = x >= 0 && x < P.V;
+            bad = i < count && !in;
+            if (in && i < count) {
                 const float p = prob(static_cast<const T*>(P.target), ((size_t)n * (P.D + 1) + i) * P.V + x);
                 const float q = P.draft ? prob(static_cast<const T*>(P.draft), at * P.V + x) : 1.0f;
-                keep = __fmul_rn(P.uniform[at], q) < p;
+                keep = __fmul_rn(u, q) < p;
             }
         }
-        if (__any_sync(0xFFFFFFFFu, bad)) return -1;
+        if (__any_sync(0xFFFFFFFFu, bad) || count < 0 || count > P.D) return -1;
         const unsigned lost = __ballot_sync(0xFFFFFFFFu, !keep);
         if (lost) return first + __ffs(lost) - 1;
+        if (first + 32 >= count) break;
     }
-    return count;
+    return count < 0 || count > P.D ? -1 : count;
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kVerThreads) verify_kernel(VerifyProblem P) {
-    __shared__ int s_kept, s_count;
-    __shared__ unsigned long long s_best[kVerThreads / 32];
-    const int n = blockIdx.x, tid = threadIdx.x, lane = tid & 31;
-    if (tid < 32) {
-        int count;
-        const int kept = drafts_kept<T>(P, n, lane, count);
-        if (lane == 0) {
-            s_kept = kept;
-            s_count = count;
-        }
-    }
-    __syncthreads();
-    const int a = s_kept;
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;\n" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;\n" ::: "memory"); }
+__device__ __forceinline__ unsigned cluster_rank() {
+    unsigned r;
+    asm("mov.u32 %0, %%cluster_ctarank;\n" : "=r"(r));
+    return r;
+}
+// writes to the same variable of another CTA of the cluster
+__device__ __forceinline__ void put(unsigned long long* p, unsigned rank, unsigned long long x) {
+    const unsigned at = (unsigned)__cvta_generic_to_shared(p);
+    asm volatile("{\n .reg .b32 a;\n mapa.shared::cluster.u32 a, %0, %1;\n st.shared::cluster.u64 [a], %2;\n}\n" ::"r"(at), "r"(rank), "l"(x) : "memory");
+}
+
+// One cluster per sequence; its CTAs take VEC elements per thread in turn and exchange their
+// winners.  Every warp decides for itself which drafts are kept, with the first noise on its way.
+template <typename T, int VEC>
+__global__ void __launch_bounds__(kVerThreads, 2) verify_kernel(VerifyProblem P, int split) {
+    constexpr int kUnits = 8 / VEC;            // of a thread at a time
+    __shared__ unsigned long long s_best[2][kVerThreads / 32], s_rank[2][kMaxSplit];
+    const int n = blockIdx.x / split, tid = threadIdx.x, lane = tid & 31;
+    const unsigned rank = cluster_rank();
+    cluster_arrive();                          // all CTAs have begun before one writes to another
+    const int units = P.V / VEC, step = split * kVerThreads, begin = (int)rank * kVerThreads + tid;
+    using Noise = Unit<float, VEC>;
+    using Prob = Unit<T, VEC>;
+    const Noise* e = reinterpret_cast<const Noise*>(P.noise + (size_t)n * P.V);
+    Noise ev[kUnits];
+    const auto noise = [&](int base) {
+#pragma unroll
+        for (int j = 0; j < kUnits; ++j)
+            if (base + j * step < units) ev[j] = e[base + j * step];
+    };
+    noise(begin);
+    int count;
+    const int a = drafts_kept<T>(P, n, lane, count);
+    cluster_wait();
     if (a < 0) {
-        if (tid == 0) set_error(P.err, KDA_ERR_BAD_INDEX);
+        if (rank == 0 && tid == 0) set_error(P.err, KDA_ERR_BAD_INDEX);
         return;
     }
-    const bool redraw = a < s_count;
-    const T* p = static_cast<const T*>(P.target) + ((size_t)n * (P.D + 1) + a) * P.V;
-    const T* q = redraw && P.draft ? static_cast<const T*>(P.draft) + ((size_t)n * P.D + a) * P.V : nullptr;
+    const bool redraw = a < count;
+    const Prob* p = reinterpret_cast<const Prob*>(static_cast<const T*>(P.target) + ((size_t)n * (P.D + 1) + a) * P.V);
+    const Prob* q = redraw && P.draft ? reinterpret_cast<const Prob*>(static_cast<const T*>(P.draft) + ((size_t)n * P.D + a) * P.V) : nullptr;
     const int sure = redraw && !P.draft ? P.tokens[(size_t)n * P.D + a] : -1;   // certain draft: q = 1 there
-    const float* e = P.noise + (size_t)n * P.V;
     unsigned long long best = 0;
+    float top = 0.0f;                          // best's score
     // a second round, on p itself, where the first finds nothing left (p nowhere above q)
     for (int round = 0; round < 2; ++round) {
-        for (int v = tid; v < P.V; v += kVerThreads) {
-            const float pv = prob(p, v);
-            const float qv = round ? 0.0f : q ? prob(q, v) : v == sure ? 1.0f : 0.0f;
-            best = max_key(best, race_key(pv - qv, e[v], v));
+        for (int base = begin; base < units; base += kUnits * step) {
+            Prob pv[kUnits], qv[kUnits];
+#pragma unroll
+            for (int j = 0; j < kUnits; ++j) {
+                const int u = base + j * step;
+                if (u < units) {
+                    pv[j] = p[u];
+                    if (q && !round) qv[j] = q[u];
+                }
+            }
+            if (round || base != begin) noise(base);
+#pragma unroll
+            for (int j = 0; j < kUnits; ++j) {
+                if (base + j * step >= units) break;
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) {
+                    const int v = (base + j * step) * VEC + i;
+                    float rest = prob(pv[j].v, i);
+                    if (!round) rest -= q ? prob(qv[j].v, i) : v == sure ? 1.0f : 0.0f;
+                    // the division only where the score may be above the thread's best: the product
+                    // is below best x noise by more than its roundings, and far from underflow
+                    const float least = top * ev[j].v[i] * 0.999999f;
+                    if (rest <= least && least > 1e-30f) continue;
+                    const unsigned long long key = race_key(rest, ev[j].v[i], v);
+                    if (key > best) {
+                        best = key;
+                        top = __uint_as_float((unsigned)(key >> 32));
+                    }
+                }
+            }
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) best = max_key(best, __shfl_xor_sync(0xFFFFFFFFu, best, o));
-        if (lane == 0) s_best[tid >> 5] = best;
+        if (lane == 0) s_best[round][tid >> 5] = best;
         __syncthreads();
+        if (tid < 32) {
+            best = lane < kVerThreads / 32 ? s_best[round][lane] : 0ull;
 #pragma unroll
-        for (int i = 0; i < kVerThreads / 32; ++i) best = max_key(best, s_best[i]);
+            for (int o = 16; o > 0; o >>= 1) best = max_key(best, __shfl_xor_sync(0xFFFFFFFFu, best, o));
+            if (lane < split) put(&s_rank[round][rank], lane, best);
+        }
+        cluster_arrive();
+        cluster_wait();
+        best = 0;
+        for (int i = 0; i < split; ++i) best = max_key(best, s_rank[round][i]);
         if (best || !redraw) break;
-        __syncthreads();
     }
+    if (rank) return;
     if (tid == 0) P.accepted[n] = a;
     int* out = P.result + (size_t)n * (P.D + 1);
     for (int i = tid; i <= P.D; i += kVerThreads)
         out[i] = i < a ? P.tokens[(size_t)n * P.D + i] : i == a && best ? (int)~(unsigned)best : -1;
+}
+
+template <typename T, int VEC>
+cudaError_t launch(const VerifyProblem& P, int split, cudaStream_t s) {
+    static const cudaError_t allowed =         // clusters of more than 8 CTAs
+        cudaFuncSetAttribute(verify_kernel<T, VEC>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (allowed != cudaSuccess) return allowed;
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim = {(unsigned)split, 1, 1};
+    cfg.gridDim = dim3((unsigned)(P.N * split));
+    cfg.blockDim = dim3(kVerThreads);
+    cfg.stream = s;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, verify_kernel<T, VEC>, P, split);
+}
+
+// CTAs per sequence: twice the SMs in all if the rows are long enough for that
+int split_of(int N, int V, int sms) {
+    int split = 1;
+    while (split < kMaxSplit && (long long)N * split * 2 <= 2LL * sms && (long long)V >= (long long)split * 2 * kMinSlice) split *= 2;
+    return split;
+}
+
+template <typename T>
+cudaError_t launch(const VerifyProblem& P, int sms, cudaStream_t s) {
+    const int split = split_of(P.N, P.V, sms);
+    // four elements at a time where every row begins on that boundary
+    if (P.V % 4 == 0 && aligned16(P.noise) && reinterpret_cast<uintptr_t>(P.target) % (4 * sizeof(T)) == 0 &&
+        reinterpret_cast<uintptr_t>(P.draft) % (4 * sizeof(T)) == 0)
+        return launch<T, 4>(P, split, s);
+    return launch<T, 1>(P, split, s);
 }
 
 }  // namespace
@@ -151,18 +247,16 @@ extern "C" int kda_verify_drafts(const void* target_probs, const void* draft_pro
             if (overlaps(out_p[o], out_n[o], in_p[i], in_n[i])) return KDA_ERR_ALIAS;
     }
     if (overlaps(accepted, out_n[0], tokens, out_n[1])) return KDA_ERR_ALIAS;
-    int dev = 0;
+    int dev = 0, sms = 0;
     int* err = nullptr;
-    const int rc = device_setup(&dev, &err);
+    const int rc = device_setup(&dev, &err, &sms);
     if (rc != KDA_OK) return rc;
     if (N == 0) return KDA_OK;
     VerifyProblem P{target_probs, draft_probs, draft_tokens, uniform, noise, num_drafts,
                     accepted, tokens, N, D, V, err};
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const cudaError_t e = timed_launch(KDA_KERNEL_VERIFY, s, [&] {
-        if (dtype == KDA_BF16) verify_kernel<__nv_bfloat16><<<N, kVerThreads, 0, s>>>(P);
-        else verify_kernel<float><<<N, kVerThreads, 0, s>>>(P);
-        return cudaGetLastError();
+        return dtype == KDA_BF16 ? launch<__nv_bfloat16>(P, sms, s) : launch<float>(P, sms, s);
     });
     if (e != cudaSuccess) return cuda_fail(KDA_ERR_LAUNCH, e);
     return KDA_OK;
