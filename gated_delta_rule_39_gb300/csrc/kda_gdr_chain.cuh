@@ -77,15 +77,19 @@ __device__ inline void keys(const GdrChunked& P, const CUtensorMap& vmap, ChainS
         prefetch_l2(block + c * step + 128 * p);                               // T beta and P
         if (p < 8) prefetch_l2(block + c * step + 2 * kTileBytes + 128 * p);   // gates
     };
+    // no copy is on its way when the warp that started it leaves
+    const auto leave = [&](int begun) {
+        if (p < 32)
+            for (int c = max(0, begun - kStages); c < begun; ++c) bar_wait(&S.copied[c % kStages], (unsigned)((c / kStages) & 1), P.err);
+    };
     k.fetch(0);
     float ga = gate[0];
     ahead(1);
     ahead(2);
     for (int c = 0; c < nch; ++c) {
         const int st = c % kStages, rows = min(kC, span.len - c * kC);
-        const unsigned phase = (unsigned)((c / kStages) & 1);
         auto& G = S.stage[st];
-        if (c >= kStages && !bar_wait(&S.empty[st], phase ^ 1u, P.err)) return;
+        if (c >= kStages && !bar_wait(&S.empty[st], (unsigned)((c / kStages) & 1) ^ 1u, P.err)) return leave(c);
         if (p == 0) {
             const uint32_t bar = smem_u32(&S.copied[st]);
             tc::mbar_arrive_expect_tx(bar, 2 * kTileBytes + (rows == kC ? kRowsTile : 0));
@@ -110,8 +114,6 @@ __device__ inline void keys(const GdrChunked& P, const CUtensorMap& vmap, ChainS
                     row0 + 8 * i < rows ? __ldg(reinterpret_cast<const uint4*>(v + 8 * i * I.v_stride)) : make_uint4(0u, 0u, 0u, 0u);
         }
         tc::fence_proxy_async_smem();         // the MMAs read what was stored here
-        // `full` means the copies too; and no copy is on its way when this warp leaves
-        if (p < 32) bar_wait(&S.copied[st], phase, P.err);
         bar_arrive(&S.full[st]);
         if (c + 1 < nch) {
             k.fetch(c + 1);
@@ -119,6 +121,7 @@ __device__ inline void keys(const GdrChunked& P, const CUtensorMap& vmap, ChainS
         }
         ahead(c + 3);
     }
+    leave(nch);
 }
 
 __device__ inline void queries(const GdrChunked& P, ChainSmem& S, const Span& span, int nch, int h, int p) {
@@ -158,7 +161,10 @@ __device__ void issue(const GdrChunked& P, ChainSmem& S, int nch, uint32_t tmem)
         tc::fence_after_sync();
         return ok;
     };
-    const auto there = [&](int c) { return wait(S.full[c % kStages], (unsigned)((c / kStages) & 1)); };
+    const auto there = [&](int c) {
+        const unsigned phase = (unsigned)((c / kStages) & 1);
+        return wait(S.copied[c % kStages], phase) && wait(S.full[c % kStages], phase);
+    };
     // R^T's part that does not need the state: V^T I
     const auto begin = [&](int c) {
         const uint32_t on = tc::elect();

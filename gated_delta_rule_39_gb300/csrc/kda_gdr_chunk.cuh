@@ -80,11 +80,6 @@ __device__ __forceinline__ void bar_init(uint64_t* b, int count) {
 __device__ __forceinline__ void bar_arrive(uint64_t* b) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(smem_u32(b)) : "memory");
 }
-// a 16-byte copy that is a zero where `there` is false
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool there) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void copies_landed() { asm volatile("cp.async.wait_all;\n" ::: "memory"); }
 // Waits, as a whole warp, for a phase to end; after KDA_WAIT_TRIES tries (each of which sleeps
 // for up to 20 us, as the hardware sees fit) records a timeout and gives up.  Every lane gets
 // the same answer.  Kept short: it is part of every role's loop.
