@@ -237,8 +237,8 @@ int kda_gdr_bwd(const void* q, const void* k, const void* v, const void* g, cons
         for (int o2 = o + 1; o2 < 6; ++o2)
             if (overlaps(out_p[o], out_n[o], out_p[o2], out_n[o2])) return KDA_ERR_ALIAS;
     }
-    int dev = 0;
-    rc = device_setup(&dev, &P.fwd.err);
+    int dev = 0, sms = 0;
+    rc = device_setup(&dev, &P.fwd.err, &sms);
     if (rc != KDA_OK) return rc;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const BwdLayout L = bwd_layout(varlen, B, T, Hk, Hv, N);
@@ -278,7 +278,7 @@ int kda_gdr_bwd(const void* q, const void* k, const void* v, const void* g, cons
     if (e == cudaSuccess)
         e = timed_launch(KDA_KERNEL_GDR_BWD_CHAIN, s, [&] { return launch_gdr_bwd_chain(P, s); });
     if (e == cudaSuccess)
-        e = timed_launch(KDA_KERNEL_GDR_BWD_CHUNK, s, [&] { return launch_gdr_bwd_chunk(P, s); });
+        e = timed_launch(KDA_KERNEL_GDR_BWD_CHUNK, s, [&] { return launch_gdr_bwd_chunk(P, sms, s); });
     cudaFreeAsync(scratch, s);
     if (e != cudaSuccess) return cuda_fail(KDA_ERR_LAUNCH, e);
     return KDA_OK;

@@ -24,6 +24,8 @@
 // key head) (grad_scale) and scale folded into dO; sums and states are fp32.  Gradients of
 // queries and keys that a group of value heads shares are summed in registers by one CTA, in a
 // fixed order.
+#include <algorithm>
+
 #include "kda_gdr_chunk.cuh"
 
 namespace kda {
@@ -34,7 +36,7 @@ using namespace gdr;
 // ---- the largest incoming gradient of each (sequence, key head) ---------------------------
 constexpr int kAmaxThreads = 256;
 
-// one CTA per (chunk, key head): dO of the chunk's tokens; chunk 0 also takes the states'
+// one CTA per (chunk, key head): dO of the chunk's tokens and a share of the last state's gradient
 __global__ void __launch_bounds__(kAmaxThreads) gdr_amax_kernel(GdrBackward B) {
     const GdrInputs& I = B.fwd.in;
     int n, c;
@@ -47,51 +49,70 @@ __global__ void __launch_bounds__(kAmaxThreads) gdr_amax_kernel(GdrBackward B) {
     const auto take = [](unsigned u, unsigned& m) {   // two bf16 values; NaN compares above infinity
         m = max(m, max(u & 0x7FFF0000u, (u & 0x7FFFu) << 16));
     };
-    for (int i = tid; i < rows * units; i += kAmaxThreads) {
-        const uint4 u = *reinterpret_cast<const uint4*>(src + (size_t)(i / units) * I.Hv * kDim + (i % units) * 8);
-        take(u.x, top); take(u.y, top); take(u.z, top); take(u.w, top);
+    for (int at = tid & 31; at < units; at += 32) {
+#pragma unroll
+        for (int i = 0; i < kC; i += kAmaxThreads / 32) {
+            const int row = i + (tid >> 5);
+            uint4 u = make_uint4(0u, 0u, 0u, 0u);
+            if (row < rows) u = __ldg(reinterpret_cast<const uint4*>(src + (size_t)row * I.Hv * kDim + at * 8));
+            take(u.x, top); take(u.y, top); take(u.z, top); take(u.w, top);
+        }
     }
     top = __float_as_uint(fabsf(I.scale) * __uint_as_float(top));
     unsigned dfinal_top = 0;
-    if (c == 0 && B.dfinal) {
+    if (B.dfinal) {
         const size_t base = ((size_t)n * I.Hv + hk * share) * kDim * kDim, count = (size_t)share * kDim * kDim;
-        if (B.dfinal_dtype == KDA_F32) {
-            const uint4* p = reinterpret_cast<const uint4*>(static_cast<const float*>(B.dfinal) + base);
-            for (size_t i = tid; i < count / 4; i += kAmaxThreads) {
-                const uint4 u = p[i];
-                dfinal_top = max(dfinal_top, max(max(u.x & 0x7FFFFFFFu, u.y & 0x7FFFFFFFu), max(u.z & 0x7FFFFFFFu, u.w & 0x7FFFFFFFu)));
-            }
-        } else {
-            const uint4* p = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(B.dfinal) + base);
-            for (size_t i = tid; i < count / 8; i += kAmaxThreads) {
-                const uint4 u = p[i];
-                take(u.x, dfinal_top); take(u.y, dfinal_top); take(u.z, dfinal_top); take(u.w, dfinal_top);
+        const size_t first = (size_t)c * kAmaxThreads + tid, step = (size_t)((span.len + kC - 1) / kC) * kAmaxThreads;
+        const bool f32 = B.dfinal_dtype == KDA_F32;
+        const size_t per = f32 ? 4 : 8;        // values of 16 bytes
+        const uint4* p = reinterpret_cast<const uint4*>(static_cast<const unsigned char*>(B.dfinal) + base * (16 / per));
+        for (size_t i = first; i < count / per; i += 8 * step) {
+            uint4 u[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) u[j] = i + j * step < count / per ? __ldg(p + i + j * step) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                if (f32) {
+                    dfinal_top = max(dfinal_top, max(max(u[j].x & 0x7FFFFFFFu, u[j].y & 0x7FFFFFFFu), max(u[j].z & 0x7FFFFFFFu, u[j].w & 0x7FFFFFFFu)));
+                } else {
+                    take(u[j].x, dfinal_top); take(u[j].y, dfinal_top); take(u[j].z, dfinal_top); take(u[j].w, dfinal_top);
+                }
             }
         }
     }
+    __shared__ unsigned s_top;
+    if (tid == 0) s_top = 0;
+    __syncthreads();
     top = __reduce_max_sync(0xFFFFFFFFu, max(top, dfinal_top));
+    if ((tid & 31) == 0) atomicMax(&s_top, top);
+    __syncthreads();
     // a maximum does not depend on the order of the atomics
-    if ((tid & 31) == 0) atomicMax(&B.amax[(size_t)n * I.Hk + hk], top);
+    if (tid == 0) atomicMax(&B.amax[(size_t)n * I.Hk + hk], s_top);
 }
 
 // ---- chunk by chunk ---------------------------------------------------------------------------
-// One CTA of 8 warps per (chunk, key head), which walks the group's value heads.  Warp w
-// forms rows (tokens) 16 (w & 3) .. of dQ and dK for the key channels 64 (w >> 2) .., and
-// the columns 32 (w >> 2) .. of the token-by-token products.
-constexpr int kChunkThreads = 256;
+// One CTA of 16 warps per (chunk, key head), which walks the group's value heads.  Warp w
+// forms rows (tokens) 16 (w & 3) .. of dQ and dK for the key channels 32 (w >> 2) .., and
+// the columns 16 (w >> 2) .. of the token-by-token products.  The CTAs, one per SM, walk the
+// (chunk, key head) pairs with a stride; a head's tiles are fetched while the one before is worked on, each
+// as soon as its place is free (without that, waiting for them took 40 % of the time).
+constexpr int kChunkThreads = 512, kParts = kChunkThreads / 128;
+
+constexpr int kPairBytes = kBlockUsed - kTileBytes;   // of a block, from P on
 
 struct ChunkSmem {
-    __align__(128) unsigned char k[kC * kDim * 2];   // fp16, 256-byte rows
-    __align__(128) unsigned char q[kC * kDim * 2];
+    __align__(128) unsigned char k[2][kC * kDim * 2];   // fp16, 256-byte rows; this pair's and the next one's
+    __align__(128) unsigned char q[2][kC * kDim * 2];
     __align__(128) unsigned char o[kC * kDim * 2];   // dO, fp16, scaled
     __align__(128) unsigned char s[kStateTile];      // S^T (rows in units, as kept in memory)
     __align__(128) unsigned char ds[kStateTile];     // dS^T
     __align__(128) unsigned char x[kTokenTile];      // X^T
     __align__(128) unsigned char y[kTokenTile];      // Y^T
-    __align__(128) unsigned char block[kBlockBytes]; // T (then dP), P (then dB), gates
-    float row[5][2][kC];      // sums over channels or columns, one slot per half
+    __align__(128) unsigned char pg[2][(kPairBytes + 127) / 128 * 128];   // P, gates; this head's and the next one's
+    __align__(128) unsigned char dp[kTileBytes], db[kTileBytes];
+    float row[5][kParts][kC]; // sums over channels or columns, one slot per part
     float col[4][kC];         // column sums of dP . Q K^T + dB . K K^T, one slot per 16 rows
-    float yv[2][kC];
+    float yv[kParts][kC];
     float dot[kChunkThreads / 32];
 };
 
@@ -117,23 +138,52 @@ __device__ __forceinline__ float rows_sum(float x) {       // over the 8 rows of
     return x + __shfl_xor_sync(0xFFFFFFFFu, x, 16);
 }
 
-// 64 rows of 128 bf16 channels (zeros from row `rows` on) as a tile of fp16, times `by`
-__device__ __forceinline__ void load_half_tile(unsigned char* dst, const __nv_bfloat16* src, long long stride, int rows,
-                                               float by, int tid) {
+// 64 rows of 128 bf16 channels (zeros from row `rows` on) on their way to a tile, which the threads
+// that fetched them then turn into fp16 in place, times `by`
+__device__ __forceinline__ void fetch_rows(unsigned char* dst, const __nv_bfloat16* src, long long stride, int rows, int tid) {
 #pragma unroll
     for (int i = 0; i < kC * 16 / kChunkThreads; ++i) {
         const int unit = tid & 15, row = (tid >> 4) + i * (kChunkThreads / 16);
-        uint4 u = make_uint4(0u, 0u, 0u, 0u);
-        if (row < rows) u = __ldg(reinterpret_cast<const uint4*>(src + row * stride + unit * 8));
-        u.x = pack_half2(by * bf16_lo(u.x), by * bf16_hi(u.x));
-        u.y = pack_half2(by * bf16_lo(u.y), by * bf16_hi(u.y));
-        u.z = pack_half2(by * bf16_lo(u.z), by * bf16_hi(u.z));
-        u.w = pack_half2(by * bf16_lo(u.w), by * bf16_hi(u.w));
-        *reinterpret_cast<uint4*>(dst + row * 256 + ((unit ^ (row & 7)) << 4)) = u;
+        const bool there = row < rows;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n"
+                     ::"r"(smem_u32(dst + row * 256 + ((unit ^ (row & 7)) << 4))), "l"(src + (there ? row * stride : 0) + unit * 8),
+                       "r"(there ? 16 : 0) : "memory");
+    }
+}
+__device__ __forceinline__ void rows_to_half(unsigned char* tile, float by, int tid) {
+#pragma unroll
+    for (int i = 0; i < kC * 16 / kChunkThreads; ++i) {
+        const int unit = tid & 15, row = (tid >> 4) + i * (kChunkThreads / 16);
+        uint4& u = *reinterpret_cast<uint4*>(tile + row * 256 + ((unit ^ (row & 7)) << 4));
+        u = make_uint4(pack_half2(by * bf16_lo(u.x), by * bf16_hi(u.x)), pack_half2(by * bf16_lo(u.y), by * bf16_hi(u.y)),
+                       pack_half2(by * bf16_lo(u.z), by * bf16_hi(u.z)), pack_half2(by * bf16_lo(u.w), by * bf16_hi(u.w)));
     }
 }
 __device__ __forceinline__ void copy_tile(unsigned char* dst, const unsigned char* src, int bytes, int tid) {
     for (int i = tid; i < bytes / 16; i += kChunkThreads) cp_async16(dst + 16 * i, src + 16 * i);
+}
+
+// `bytes` (a multiple of 16) from p on into L2
+__device__ __forceinline__ void bulk_prefetch(const void* p, int bytes) {
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;\n" ::"l"(p), "r"(bytes) : "memory");
+}
+
+// A (chunk, key head) pair of the grid's walk
+struct Place {
+    int chunk, hk, rows, n;
+    long long tok;            // the chunk's first token
+};
+__device__ __forceinline__ bool place(const GdrChunked& P, int pair, Place& p) {
+    const GdrInputs& I = P.in;
+    if (pair >= P.chunks.total * I.Hk) return false;
+    int c;
+    p.chunk = pair / I.Hk;
+    p.hk = pair % I.Hk;
+    if (!find_chunk(I, P.chunks, p.chunk, p.n, c)) return false;     // nor are there any after it
+    const Span span = span_of(I, P.chunks, p.n);
+    p.tok = span.start + (long long)c * kC;
+    p.rows = min(kC, span.len - c * kC);
+    return true;
 }
 
 __device__ __forceinline__ void store_gate(void* p, int dtype, size_t i, float x) {
@@ -146,86 +196,223 @@ __global__ void __launch_bounds__(kChunkThreads, 1) gdr_bwd_chunk_kernel(GdrBack
     ChunkSmem& S = *reinterpret_cast<ChunkSmem*>(raw);
     const GdrChunked& P = B.fwd;
     const GdrInputs& I = P.in;
-    const int chunk = blockIdx.x, hk = blockIdx.y;
-    int n, c;
-    if (!find_chunk(I, P.chunks, chunk, n, c)) return;
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, g = lane >> 2, t = lane & 3;
-    const int rw = w & 3, half = w >> 2, share = I.Hv / I.Hk;
-    const Span span = span_of(I, P.chunks, n);
-    const long long tok = span.start + (long long)c * kC;
-    const int rows = min(kC, span.len - c * kC);
-    const float sigma = grad_scale(B.amax[(size_t)n * I.Hk + hk]), back = 1.0f / sigma;
-    load_half_tile(S.k, I.k + tok * I.k_stride + hk * kDim, I.k_stride, rows, 1.0f, tid);
-    load_half_tile(S.q, I.q + tok * I.q_stride + hk * kDim, I.q_stride, rows, 1.0f, tid);
-    const uint32_t sk = smem_u32(S.k), sq = smem_u32(S.q), so = smem_u32(S.o), ss = smem_u32(S.s),
-                   sds = smem_u32(S.ds), sx = smem_u32(S.x), sy = smem_u32(S.y), sT = smem_u32(S.block),
-                   sP = sT + kTileBytes;
-    const float* gate = reinterpret_cast<const float*>(S.block + 2 * kTileBytes);
+    const int rw = w & 3, part = w >> 2, share = I.Hv / I.Hk;
+    const uint32_t so = smem_u32(S.o), ss = smem_u32(S.s), sds = smem_u32(S.ds), sx = smem_u32(S.x), sy = smem_u32(S.y),
+                   sdp = smem_u32(S.dp), sdb = smem_u32(S.db);
     const int i0 = 16 * rw + g, i1 = i0 + 8;               // this lane's rows
-    float dq[8][4], dk[8][4], kk[4][4];
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) dq[j][e] = dk[j][e] = 0.0f;
-    for (int h = hk * share; h < (hk + 1) * share; ++h) {
-        const size_t at = (size_t)chunk * I.Hv + h;
+    // what the head's parts need, in the order in which their places become free
+    const auto fetch_pair = [&](const Place& p, int to) {
+        fetch_rows(S.k[to], I.k + p.tok * I.k_stride + p.hk * kDim, I.k_stride, p.rows, tid);
+        fetch_rows(S.q[to], I.q + p.tok * I.q_stride + p.hk * kDim, I.q_stride, p.rows, tid);
+    };
+    const auto fetch_gates = [&](const Place& p, int h, int to) {
+        copy_tile(S.pg[to], P.blocks + ((size_t)p.chunk * I.Hv + h) * kBlockBytes + kTileBytes, kPairBytes, tid);
+    };
+    const auto fetch_first = [&](const Place& p, int h) {
+        const size_t at = (size_t)p.chunk * I.Hv + h;
         copy_tile(S.s, P.states + at * kStateTile, kStateTile, tid);
         copy_tile(S.y, B.ys + at * kTokenTile, kTokenTile, tid);
-        copy_tile(S.block, P.blocks + at * kBlockBytes, kBlockUsed, tid);
+        fetch_rows(S.o, B.dout + (p.tok * I.Hv + h) * kDim, (long long)I.Hv * kDim, p.rows, tid);
+    };
+    const auto fetch_second = [&](const Place& p, int h) {
+        const size_t at = (size_t)p.chunk * I.Hv + h;
         copy_tile(S.ds, B.dstates + at * kStateTile, kStateTile, tid);
         copy_tile(S.x, P.xs + at * kTokenTile, kTokenTile, tid);
-        cp_async_commit();
-        load_half_tile(S.o, B.dout + (tok * I.Hv + h) * kDim, (long long)I.Hv * kDim, rows, I.scale * sigma, tid);
-        cp_async_wait<0>();
-        __syncthreads();
-        if (h == hk * share) {         // K K^T, this warp's 16 rows and 32 columns
+    };
+    // into L2, what is fetched later in this step
+    const auto prefetch = [&](const Place& p, int h) {
+        const size_t at = (size_t)p.chunk * I.Hv + h;
+        if (tid < 128) {                       // dO and V: lines of 64 channels
+            const int row = tid >> 1, ch = 64 * (tid & 1);
+            if (row < p.rows) {
+                asm volatile("prefetch.global.L2 [%0];\n" ::"l"(B.dout + ((p.tok + row) * I.Hv + h) * kDim + ch));
+                asm volatile("prefetch.global.L2 [%0];\n" ::"l"(I.v + (p.tok + row) * I.v_stride + h * kDim + ch));
+            }
+        } else if (tid == 128) {
+            bulk_prefetch(P.states + at * kStateTile, kStateTile);
+            bulk_prefetch(B.ys + at * kTokenTile, kTokenTile);
+            bulk_prefetch(B.dstates + at * kStateTile, kStateTile);
+            bulk_prefetch(P.xs + at * kTokenTile, kTokenTile);
+        }
+    };
+    Place now, next;
+    int pair = blockIdx.x, turn = 0, kq = 0;
+    if (!place(P, pair, now)) return;
+    fetch_pair(now, 0);
+    fetch_gates(now, now.hk * share, 0);
+    fetch_first(now, now.hk * share);
+    fetch_second(now, now.hk * share);
+    float dq[4][4], dk[4][4], kk[2][4];
+    for (bool more = true; more; now = next, kq ^= 1) {
+    pair += gridDim.x;
+    more = place(P, pair, next);
+    const int hk = now.hk, rows = now.rows;
+    const long long tok = now.tok;
+    const float sigma = grad_scale(B.amax[(size_t)now.n * I.Hk + hk]), back = 1.0f / sigma;
+    const uint32_t sk = smem_u32(S.k[kq]), sq = smem_u32(S.q[kq]);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) kk[j][0] = kk[j][1] = kk[j][2] = kk[j][3] = 0.0f;
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) dq[j][e] = dk[j][e] = 0.0f;
+    for (int h = hk * share; h < (hk + 1) * share; ++h, turn ^= 1) {
+        const bool last = h + 1 == (hk + 1) * share;
+        const Place& then = last ? next : now;             // where the head after this one is
+        const int then_h = last ? next.hk * share : h + 1;
+        const bool follows = !last || more;
+        const unsigned char* pg = S.pg[turn];
+        const float* gate = reinterpret_cast<const float*>(pg + kTileBytes);
+        // values for Y.V: rows i0 and i1, a quarter of the channels
+        uint32_t v[2][4];
+        const __nv_bfloat16* vp = I.v + (tok + i0) * I.v_stride + h * kDim + 32 * part + 2 * t;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int m = 0; m < 4; ++m)
+                v[i][m] = (m & 1 ? i1 : i0) < rows ? __ldg(reinterpret_cast<const uint32_t*>(vp + (m & 1 ? 8 * I.v_stride : 0) + 16 * i + 8 * (m >> 1))) : 0u;
+        asm volatile("cp.async.wait_all;\n" ::: "memory");
+        rows_to_half(S.o, I.scale * sigma, tid);
+        if (h == hk * share) {
+            rows_to_half(S.k[kq], 1.0f, tid);
+            rows_to_half(S.q[kq], 1.0f, tid);
+        }
+        __syncthreads();
+        if (follows) {
+            prefetch(then, then_h);
+            fetch_gates(then, then_h, turn ^ 1);
+            if (last) fetch_pair(next, kq ^ 1);
+        }
+        if (h == hk * share) {         // K K^T, this warp's 16 rows and 16 columns
+#pragma unroll
+            for (int j = 0; j < 2; ++j) kk[j][0] = kk[j][1] = kk[j][2] = kk[j][3] = 0.0f;
 #pragma unroll
             for (int ks = 0; ks < 8; ++ks) {
-                uint32_t a[4];
+                uint32_t a[4], b[4];
                 ldsm(a, a_addr<256>(sk, 16 * rw, 2 * ks, lane));
-#pragma unroll
-                for (int np = 0; np < 2; ++np) {
-                    uint32_t b[4];
-                    ldsm(b, b_addr<256>(sk, 32 * half + 16 * np, 2 * ks, lane));
-                    mma_f16(kk[2 * np], a, b[0], b[1]);
-                    mma_f16(kk[2 * np + 1], a, b[2], b[3]);
-                }
+                ldsm(b, b_addr<256>(sk, 16 * part, 2 * ks, lane));
+                mma_f16(kk[0], a, b[0], b[1]);
+                mma_f16(kk[1], a, b[2], b[3]);
             }
         }
         const float e0 = gate[kGateE + i0], e1 = gate[kGateE + i1];
         const float be0 = gate[kGateBe + i0], be1 = gate[kGateBe + i1];
         const float b0 = gate[kGateB + i0], b1 = gate[kGateB + i1];
-        // dO S^T and Y S^T: this warp's rows, 64 key channels, over 128 value channels
         {
-            float a[8][4], z[8][4], yv0 = 0.0f, yv1 = 0.0f;
-            const __nv_bfloat16* vp = I.v + (tok + i0) * I.v_stride + h * kDim + 2 * t;
+            float yv0 = 0.0f, yv1 = 0.0f;
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
+            for (int i = 0; i < 2; ++i) {
+                uint32_t fy[4];
+                ldsm_t(fy, row_b(sy, 32 * part + 16 * i, 2 * rw, lane));
+#pragma unroll
+                for (int m = 0; m < 4; ++m) {              // rows i0, i1; channels 2 t (+ 8)
+                    const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&fy[m]));
+                    (m & 1 ? yv1 : yv0) += y.x * bf16_lo(v[i][m]) + y.y * bf16_hi(v[i][m]);
+                }
+            }
+            yv0 = quad_sum(yv0);
+            yv1 = quad_sum(yv1);
+            if (t == 0) {
+                S.yv[part][i0] = yv0; S.yv[part][i1] = yv1;
+            }
+        }
+        // <S, dS>: the diagonal of S^T dS, rows 16 (w / 2) .. over half of the key channels
+        {
+            float d[2][4] = {};
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks) {
+                uint32_t a[4], b[4];
+                ldsm(a, row_a(ss, 16 * (w >> 1), 8 * (w & 1) + 2 * ks, lane));
+                ldsm(b, row_b(sds, 16 * (w >> 1), 8 * (w & 1) + 2 * ks, lane));
+                mma_f16(d[0], a, b[0], b[1]);
+                mma_f16(d[1], a, b[2], b[3]);
+            }
+            // rows g (and g + 8), columns 2 t, 2 t + 1 (and the same + 8)
+            float x = g == 2 * t ? d[0][0] + d[1][2] : g == 2 * t + 1 ? d[0][1] + d[1][3] : 0.0f;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, o);
+            if (lane == 0) S.dot[w] = x;
+        }
+        {
+            // dO X^T and Y X^T: this warp's 16 rows, 16 columns
+            float dp[2][4], da[2][4];
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) dp[j][e] = da[j][e] = 0.0f;
+            if (part <= rw) {              // else columns past the rows
+#pragma unroll
+                for (int ks = 0; ks < 8; ++ks) {
+                    uint32_t fo[4], fy[4], b[4];
+                    ldsm(fo, a_addr<256>(so, 16 * rw, 2 * ks, lane));
+                    ldsm_t(fy, row_b(sy, 16 * ks, 2 * rw, lane));
+                    ldsm_t(b, row_a(sx, 16 * ks, 2 * part, lane));
+                    mma_f16(dp[0], fo, b[0], b[1]);
+                    mma_f16(dp[1], fo, b[2], b[3]);
+                    mma_f16(da[0], fy, b[0], b[1]);
+                    mma_f16(da[1], fy, b[2], b[3]);
+                }
+            }
+            // dP, dB and the sums of dP . Q K^T + dB . K K^T (M . Q K^T is P)
+            uint32_t fp[2][2], fb[2][2];
+            float rs0 = 0.0f, rs1 = 0.0f, bs0 = 0.0f, bs1 = 0.0f;
+            {
+                const float g0 = gate[kGateG + i0], g1 = gate[kGateG + i1];
+#pragma unroll
+                for (int nt = 0; nt < 2; ++nt) {
+                    const int j = 16 * part + 8 * nt + 2 * t;
+                    float cs[2] = {0.0f, 0.0f}, pv[4], bv[4];
+                    const float2 gj = *reinterpret_cast<const float2*>(gate + kGateG + j);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int i = e < 2 ? i0 : i1, jj = j + (e & 1);
+                        const float m = jj <= i ? ex2_approx((e < 2 ? g0 : g1) - (e & 1 ? gj.y : gj.x)) : 0.0f;
+                        const float pq = __half2float(*reinterpret_cast<const __half*>(
+                            pg + i * 128 + (((jj >> 3) ^ (i & 7)) << 4) + (jj & 7) * 2));
+                        const float mk = jj < i ? m * kk[nt][e] : 0.0f;
+                        const float dpv = dp[nt][e], dav = -da[nt][e], bi = e < 2 ? b0 : b1;
+                        pv[e] = jj <= i ? m * dpv : 0.0f;
+                        bv[e] = jj < i ? bi * m * dav : 0.0f;
+                        const float sum = (jj <= i ? dpv * pq : 0.0f) + bi * dav * mk;
+                        cs[e & 1] += sum;
+                        (e < 2 ? rs0 : rs1) += sum;
+                        (e < 2 ? bs0 : bs1) += dav * mk;
+                    }
+                    fp[nt][0] = pack_half2(pv[0], pv[1]);
+                    fp[nt][1] = pack_half2(pv[2], pv[3]);
+                    fb[nt][0] = pack_half2(bv[0], bv[1]);
+                    fb[nt][1] = pack_half2(bv[2], bv[3]);
+                    cs[0] = rows_sum(cs[0]);
+                    cs[1] = rows_sum(cs[1]);
+                    if (g == 0) {
+                        S.col[rw][j] = cs[0];
+                        S.col[rw][j + 1] = cs[1];
+                    }
+                }
+                rs0 = quad_sum(rs0); rs1 = quad_sum(rs1); bs0 = quad_sum(bs0); bs1 = quad_sum(bs1);
+                if (t == 0) {
+                    S.row[3][part][i0] = rs0; S.row[3][part][i1] = rs1;
+                    S.row[4][part][i0] = bs0; S.row[4][part][i1] = bs1;
+                }
+            }
+            stsm(a_addr<128>(sdp, 16 * rw, 2 * part, lane), fp[0][0], fp[0][1], fp[1][0], fp[1][1]);
+            stsm(a_addr<128>(sdb, 16 * rw, 2 * part, lane), fb[0][0], fb[0][1], fb[1][0], fb[1][1]);
+        }
+        // dO S^T and Y S^T: this warp's rows, 32 key channels, over 128 value channels
+        {
+            float a[4][4], z[4][4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) a[j][e] = z[j][e] = 0.0f;
 #pragma unroll
             for (int ks = 0; ks < 8; ++ks) {
                 uint32_t fo[4], fy[4];
                 ldsm(fo, a_addr<256>(so, 16 * rw, 2 * ks, lane));
-                // Y as an A operand from Y^T: (tokens, v) blocks transposed; Y.V over half of the
-                // value channels by this warp
-                ldsm_t(fy, row_b(sy, 16 * ks, 2 * rw, lane));
-                if ((ks >> 2) == half) {
+                ldsm_t(fy, row_b(sy, 16 * ks, 2 * rw, lane));   // Y as an A operand from Y^T
 #pragma unroll
-                    for (int m = 0; m < 4; ++m) {          // rows i0, i1; channels 16 ks + 2 t (+ 8)
-                        if ((m & 1 ? i1 : i0) < rows) {
-                            const uint32_t v = __ldg(reinterpret_cast<const uint32_t*>(vp + (m & 1 ? 8 * I.v_stride : 0) + 16 * ks + 8 * (m >> 1)));
-                            const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&fy[m]));
-                            (m & 1 ? yv1 : yv0) += y.x * bf16_lo(v) + y.y * bf16_hi(v);
-                        }
-                    }
-                }
-#pragma unroll
-                for (int np = 0; np < 4; ++np) {
+                for (int np = 0; np < 2; ++np) {
                     uint32_t b[4];
-                    ldsm_t(b, row_a(ss, 16 * ks, 8 * half + 2 * np, lane));
+                    ldsm_t(b, row_a(ss, 16 * ks, 4 * part + 2 * np, lane));
                     mma_f16(a[2 * np], fo, b[0], b[1]);
                     mma_f16(a[2 * np + 1], fo, b[2], b[3]);
                     mma_f16(z[2 * np], fy, b[0], b[1]);
@@ -234,10 +421,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1) gdr_bwd_chunk_kernel(GdrBack
             }
             float qa0 = 0.0f, qa1 = 0.0f, kz0 = 0.0f, kz1 = 0.0f;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int ch = 64 * half + 8 * j + 2 * t;
-                const float2 q0 = half2_at(S.q, i0, ch), q1 = half2_at(S.q, i1, ch);
-                const float2 k0 = half2_at(S.k, i0, ch), k1 = half2_at(S.k, i1, ch);
+            for (int j = 0; j < 4; ++j) {
+                const int ch = 32 * part + 8 * j + 2 * t;
+                const float2 q0 = half2_at(S.q[kq], i0, ch), q1 = half2_at(S.q[kq], i1, ch);
+                const float2 k0 = half2_at(S.k[kq], i0, ch), k1 = half2_at(S.k[kq], i1, ch);
                 a[j][0] *= e0; a[j][1] *= e0; a[j][2] *= e1; a[j][3] *= e1;
                 qa0 += q0.x * a[j][0] + q0.y * a[j][1];
                 qa1 += q1.x * a[j][2] + q1.y * a[j][3];
@@ -248,26 +435,26 @@ __global__ void __launch_bounds__(kChunkThreads, 1) gdr_bwd_chunk_kernel(GdrBack
                 dk[j][2] -= be1 * z[j][2]; dk[j][3] -= be1 * z[j][3];
             }
             qa0 = quad_sum(qa0); qa1 = quad_sum(qa1); kz0 = quad_sum(kz0); kz1 = quad_sum(kz1);
-            yv0 = quad_sum(yv0); yv1 = quad_sum(yv1);
             if (t == 0) {
-                S.yv[half][i0] = yv0; S.yv[half][i1] = yv1;
-                S.row[0][half][i0] = qa0; S.row[0][half][i1] = qa1;
-                S.row[1][half][i0] = kz0; S.row[1][half][i1] = kz1;
+                S.row[0][part][i0] = qa0; S.row[0][part][i1] = qa1;
+                S.row[1][part][i0] = kz0; S.row[1][part][i1] = kz1;
             }
         }
+        __syncthreads();               // dP and dB are there; S, Y and dO have been read
+        if (follows) fetch_first(then, then_h);
         // X dS^T
         {
-            float a[8][4];
+            float a[4][4];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) a[j][0] = a[j][1] = a[j][2] = a[j][3] = 0.0f;
+            for (int j = 0; j < 4; ++j) a[j][0] = a[j][1] = a[j][2] = a[j][3] = 0.0f;
 #pragma unroll
             for (int ks = 0; ks < 8; ++ks) {
                 uint32_t fx[4];
                 ldsm_t(fx, row_b(sx, 16 * ks, 2 * rw, lane));
 #pragma unroll
-                for (int np = 0; np < 4; ++np) {
+                for (int np = 0; np < 2; ++np) {
                     uint32_t b[4];
-                    ldsm_t(b, row_a(sds, 16 * ks, 8 * half + 2 * np, lane));
+                    ldsm_t(b, row_a(sds, 16 * ks, 4 * part + 2 * np, lane));
                     mma_f16(a[2 * np], fx, b[0], b[1]);
                     mma_f16(a[2 * np + 1], fx, b[2], b[3]);
                 }
@@ -275,9 +462,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1) gdr_bwd_chunk_kernel(GdrBack
             const float f0 = gate[kGateEnd + i0], f1 = gate[kGateEnd + i1];
             float ka0 = 0.0f, ka1 = 0.0f;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int ch = 64 * half + 8 * j + 2 * t;
-                const float2 k0 = half2_at(S.k, i0, ch), k1 = half2_at(S.k, i1, ch);
+            for (int j = 0; j < 4; ++j) {
+                const int ch = 32 * part + 8 * j + 2 * t;
+                const float2 k0 = half2_at(S.k[kq], i0, ch), k1 = half2_at(S.k[kq], i1, ch);
                 a[j][0] *= f0; a[j][1] *= f0; a[j][2] *= f1; a[j][3] *= f1;
                 ka0 += k0.x * a[j][0] + k0.y * a[j][1];
                 ka1 += k1.x * a[j][2] + k1.y * a[j][3];
@@ -285,114 +472,27 @@ __global__ void __launch_bounds__(kChunkThreads, 1) gdr_bwd_chunk_kernel(GdrBack
             }
             ka0 = quad_sum(ka0); ka1 = quad_sum(ka1);
             if (t == 0) {
-                S.row[2][half][i0] = ka0; S.row[2][half][i1] = ka1;
+                S.row[2][part][i0] = ka0; S.row[2][part][i1] = ka1;
             }
         }
-        // <S, dS>
-        {
-            float d = 0.0f;
-            for (int i = tid; i < kStateTile / 16; i += kChunkThreads) {
-                const uint4 a = reinterpret_cast<const uint4*>(S.s)[i], b = reinterpret_cast<const uint4*>(S.ds)[i];
-                const uint32_t ua[4] = {a.x, a.y, a.z, a.w}, ub[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&ua[j]));
-                    const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&ub[j]));
-                    d += x.x * y.x + x.y * y.y;
-                }
-            }
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xFFFFFFFFu, d, o);
-            if (lane == 0) S.dot[w] = d;
-        }
-        // dO X^T and Y X^T: this warp's 16 rows, 32 columns
-        float dp[4][4], da[4][4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) dp[j][e] = da[j][e] = 0.0f;
-#pragma unroll
-        for (int ks = 0; ks < 8; ++ks) {
-            uint32_t fo[4], fy[4];
-            ldsm(fo, a_addr<256>(so, 16 * rw, 2 * ks, lane));
-            ldsm_t(fy, row_b(sy, 16 * ks, 2 * rw, lane));
-#pragma unroll
-            for (int np = 0; np < 2; ++np) {
-                if (2 * half + np > rw) break;             // columns past the rows
-                uint32_t b[4];
-                ldsm_t(b, row_a(sx, 16 * ks, 4 * half + 2 * np, lane));
-                mma_f16(dp[2 * np], fo, b[0], b[1]);
-                mma_f16(dp[2 * np + 1], fo, b[2], b[3]);
-                mma_f16(da[2 * np], fy, b[0], b[1]);
-                mma_f16(da[2 * np + 1], fy, b[2], b[3]);
-            }
-        }
-        // dP, dB and the sums of dP . Q K^T + dB . K K^T (M . Q K^T is P)
-        uint32_t fp[4][2], fb[4][2];
-        float rs0 = 0.0f, rs1 = 0.0f, bs0 = 0.0f, bs1 = 0.0f;
-        {
-            const float g0 = gate[kGateG + i0], g1 = gate[kGateG + i1];
-#pragma unroll
-            for (int nt = 0; nt < 4; ++nt) {
-                const int j = 32 * half + 8 * nt + 2 * t;
-                float cs[2] = {0.0f, 0.0f}, pv[4], bv[4];
-                const float2 gj = *reinterpret_cast<const float2*>(gate + kGateG + j);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int i = e < 2 ? i0 : i1, jj = j + (e & 1);
-                    const float m = jj <= i ? ex2_approx((e < 2 ? g0 : g1) - (e & 1 ? gj.y : gj.x)) : 0.0f;
-                    const float pq = __half2float(*reinterpret_cast<const __half*>(
-                        S.block + kTileBytes + i * 128 + (((jj >> 3) ^ (i & 7)) << 4) + (jj & 7) * 2));
-                    const float mk = jj < i ? m * kk[nt][e] : 0.0f;
-                    const float dpv = dp[nt][e], dav = -da[nt][e], bi = e < 2 ? b0 : b1;
-                    pv[e] = jj <= i ? m * dpv : 0.0f;
-                    bv[e] = jj < i ? bi * m * dav : 0.0f;
-                    const float sum = (jj <= i ? dpv * pq : 0.0f) + bi * dav * mk;
-                    cs[e & 1] += sum;
-                    (e < 2 ? rs0 : rs1) += sum;
-                    (e < 2 ? bs0 : bs1) += dav * mk;
-                }
-                fp[nt][0] = pack_half2(pv[0], pv[1]);
-                fp[nt][1] = pack_half2(pv[2], pv[3]);
-                fb[nt][0] = pack_half2(bv[0], bv[1]);
-                fb[nt][1] = pack_half2(bv[2], bv[3]);
-                cs[0] = rows_sum(cs[0]);
-                cs[1] = rows_sum(cs[1]);
-                if (g == 0) {
-                    S.col[rw][j] = cs[0];
-                    S.col[rw][j + 1] = cs[1];
-                }
-            }
-            rs0 = quad_sum(rs0); rs1 = quad_sum(rs1); bs0 = quad_sum(bs0); bs1 = quad_sum(bs1);
-            if (t == 0) {
-                S.row[3][half][i0] = rs0; S.row[3][half][i1] = rs1;
-                S.row[4][half][i0] = bs0; S.row[4][half][i1] = bs1;
-            }
-        }
-        __syncthreads();               // P has been read
-        // dP over T, dB over P (both lower triangles, zeros above)
-#pragma unroll
-        for (int np = 0; np < 2; ++np) {
-            stsm(a_addr<128>(sT, 16 * rw, 4 * half + 2 * np, lane), fp[2 * np][0], fp[2 * np][1], fp[2 * np + 1][0], fp[2 * np + 1][1]);
-            stsm(a_addr<128>(sP, 16 * rw, 4 * half + 2 * np, lane), fb[2 * np][0], fb[2 * np][1], fb[2 * np + 1][0], fb[2 * np + 1][1]);
-        }
-        __syncthreads();
+        __syncthreads();               // dS and X have been read, all sums are there
+        if (follows) fetch_second(then, then_h);
         // dQ += dP K, dK += dP^T Q + dB K + dB^T K
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks) {
             uint32_t fpn[4], fbn[4], fpt[4], fbt[4];
             if (ks <= rw) {            // rows reach tokens up to their own
-                ldsm(fpn, a_addr<128>(sT, 16 * rw, 2 * ks, lane));
-                ldsm(fbn, a_addr<128>(sP, 16 * rw, 2 * ks, lane));
+                ldsm(fpn, a_addr<128>(sdp, 16 * rw, 2 * ks, lane));
+                ldsm(fbn, a_addr<128>(sdb, 16 * rw, 2 * ks, lane));
             }
             if (ks >= rw) {            // transposed: from their own on
-                ldsm_t(fpt, b_addr<128>(sT, 16 * ks, 2 * rw, lane));
-                ldsm_t(fbt, b_addr<128>(sP, 16 * ks, 2 * rw, lane));
+                ldsm_t(fpt, b_addr<128>(sdp, 16 * ks, 2 * rw, lane));
+                ldsm_t(fbt, b_addr<128>(sdb, 16 * ks, 2 * rw, lane));
             }
 #pragma unroll
-            for (int np = 0; np < 4; ++np) {
+            for (int np = 0; np < 2; ++np) {
                 uint32_t b[4];
-                ldsm_t(b, a_addr<256>(sk, 16 * ks, 8 * half + 2 * np, lane));
+                ldsm_t(b, a_addr<256>(sk, 16 * ks, 4 * part + 2 * np, lane));
                 if (ks <= rw) {
                     mma_f16(dq[2 * np], fpn, b[0], b[1]);
                     mma_f16(dq[2 * np + 1], fpn, b[2], b[3]);
@@ -402,7 +502,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) gdr_bwd_chunk_kernel(GdrBack
                 if (ks >= rw) {
                     mma_f16(dk[2 * np], fbt, b[0], b[1]);
                     mma_f16(dk[2 * np + 1], fbt, b[2], b[3]);
-                    ldsm_t(b, a_addr<256>(sq, 16 * ks, 8 * half + 2 * np, lane));
+                    ldsm_t(b, a_addr<256>(sq, 16 * ks, 4 * part + 2 * np, lane));
                     mma_f16(dk[2 * np], fpt, b[0], b[1]);
                     mma_f16(dk[2 * np + 1], fpt, b[2], b[3]);
                 }
@@ -414,11 +514,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1) gdr_bwd_chunk_kernel(GdrBack
 #pragma unroll
             for (int m = 0; m < 2; ++m) {
                 const int j = 2 * lane + m;
-                const float qa = S.row[0][0][j] + S.row[0][1][j], kz = S.row[1][0][j] + S.row[1][1][j];
-                ka[m] = S.row[2][0][j] + S.row[2][1][j];
-                const float rs = S.row[3][0][j] + S.row[3][1][j], bs = S.row[4][0][j] + S.row[4][1][j];
+                const auto parts = [&](const float (&x)[kParts][kC]) { return (x[0][j] + x[1][j]) + (x[2][j] + x[3][j]); };
+                const float qa = parts(S.row[0]), kz = parts(S.row[1]), rs = parts(S.row[3]), bs = parts(S.row[4]), yv = parts(S.yv);
+                ka[m] = parts(S.row[2]);
                 const float cs = S.col[0][j] + S.col[1][j] + S.col[2][j] + S.col[3][j];
-                const float yv = S.yv[0][j] + S.yv[1][j];
                 dgv[m] = qa - ka[m] - gate[kGateBe + j] * kz + rs - cs;
                 if (j < rows)
                     store_gate(B.dbeta, I.gate_dtype, (size_t)(tok + j) * I.Hv + h,
@@ -441,12 +540,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1) gdr_bwd_chunk_kernel(GdrBack
             if (2 * lane + 1 < rows)
                 store_gate(B.dg, I.gate_dtype, (size_t)(tok + 2 * lane + 1) * I.Hv + h, back * (x - dgv[0]));
         }
-        __syncthreads();               // the tiles are free for the next head
     }
     // dQ and dK as bf16 rows
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const int ch = 64 * half + 8 * j + 2 * t;
+    for (int j = 0; j < 4; ++j) {
+        const int ch = 32 * part + 8 * j + 2 * t;
         if (i0 < rows) {
             const size_t o = ((size_t)(tok + i0) * I.Hk + hk) * kDim + ch;
             *reinterpret_cast<uint32_t*>(B.dq + o) = pack_bf16(back * dq[j][0], back * dq[j][1]);
@@ -458,6 +556,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) gdr_bwd_chunk_kernel(GdrBack
             *reinterpret_cast<uint32_t*>(B.dk + o) = pack_bf16(back * dk[j][2], back * dk[j][3]);
         }
     }
+    }
 }
 
 }  // namespace
@@ -468,11 +567,12 @@ cudaError_t launch_gdr_amax(const GdrBackward& B, cudaStream_t s) {
     return cudaGetLastError();
 }
 
-cudaError_t launch_gdr_bwd_chunk(const GdrBackward& B, cudaStream_t s) {
+cudaError_t launch_gdr_bwd_chunk(const GdrBackward& B, int sms, cudaStream_t s) {
     if (B.fwd.chunks.total == 0) return cudaSuccess;
     const cudaError_t e = allow_smem<gdr_bwd_chunk_kernel>(sizeof(ChunkSmem));
     if (e != cudaSuccess) return e;
-    gdr_bwd_chunk_kernel<<<dim3(B.fwd.chunks.total, B.fwd.in.Hk), kChunkThreads, sizeof(ChunkSmem), s>>>(B);
+    const long long pairs = (long long)B.fwd.chunks.total * B.fwd.in.Hk;
+    gdr_bwd_chunk_kernel<<<(unsigned)std::min<long long>(pairs, sms), kChunkThreads, sizeof(ChunkSmem), s>>>(B);
     return cudaGetLastError();
 }
 
