@@ -32,12 +32,12 @@ _LIB_PATH = os.path.join(_HERE, "_lib", "libkda.so")
 
 KDA_BF16 = 0
 KDA_F32 = 1
-KDA_NUM_KERNELS = 20
+KDA_NUM_KERNELS = 19
 KERNEL_NAMES = ("seqmap_kernel", "fused_kernel", "decode_kernel", "combine_kernel",
                 "segprep_kernel", "segfinal_kernel", "bwd_kernel", "bwd_finish_kernel",
                 "bwd_reduce_kernel", "qk_norm_kernel", "qk_norm_bwd_kernel",
                 "qk_norm_dw_kernel", "verify_kernel", "gdr_step_kernel",
-                "gdr_map_kernel", "gdr_prep_kernel", "gdr_chain_kernel", "gdr_amax_kernel",
+                "gdr_map_kernel", "gdr_prep_kernel", "gdr_chain_kernel",
                 "gdr_bwd_chain_kernel", "gdr_bwd_chunk_kernel")
 
 _lib = None

@@ -936,7 +936,6 @@ const char* kda_kernel_name(int kernel_id) {
         case KDA_KERNEL_GDR_MAP: return "gdr_map_kernel";
         case KDA_KERNEL_GDR_PREP: return "gdr_prep_kernel";
         case KDA_KERNEL_GDR_CHAIN: return "gdr_chain_kernel";
-        case KDA_KERNEL_GDR_AMAX: return "gdr_amax_kernel";
         case KDA_KERNEL_GDR_BWD_CHAIN: return "gdr_bwd_chain_kernel";
         case KDA_KERNEL_GDR_BWD_CHUNK: return "gdr_bwd_chunk_kernel";
         default: return "unknown";

@@ -252,10 +252,10 @@ int kda_gdr_bwd(const void* q, const void* k, const void* v, const void* g, cons
     P.fwd.init_dtype = initial_state_dtype;
     P.fwd.states = scratch + L.states;
     P.fwd.xs = scratch + L.xs;
-    P.dout = static_cast<const __nv_bfloat16*>(d_out);
-    P.dfinal = d_final_state;
-    P.dfinal_dtype = d_final_state_dtype;
-    P.amax = reinterpret_cast<unsigned*>(scratch + L.amax);
+    P.in.dout = static_cast<const __nv_bfloat16*>(d_out);
+    P.in.dfinal = d_final_state;
+    P.in.dfinal_dtype = d_final_state_dtype;
+    P.in.amax = reinterpret_cast<unsigned*>(scratch + L.amax);
     P.dstates = scratch + L.dstates;
     P.ys = scratch + L.ys;
     P.dq = static_cast<__nv_bfloat16*>(dq);
@@ -272,9 +272,8 @@ int kda_gdr_bwd(const void* q, const void* k, const void* v, const void* g, cons
         e = timed_launch(KDA_KERNEL_GDR_MAP, s,
                          [&] { return launch_gdr_map(in, first, first + N + 1, P.fwd.err, s); });
     }
-    if (e == cudaSuccess) e = cudaMemsetAsync(P.amax, 0, (size_t)N * Hk * 4, s);
-    if (e == cudaSuccess) e = timed_launch(KDA_KERNEL_GDR_AMAX, s, [&] { return launch_gdr_amax(P, s); });
-    if (e == cudaSuccess) e = timed_launch(KDA_KERNEL_GDR_PREP, s, [&] { return launch_gdr_prep(P.fwd, s); });
+    if (e == cudaSuccess) e = cudaMemsetAsync(P.in.amax, 0, (size_t)N * Hk * 4, s);
+    if (e == cudaSuccess) e = timed_launch(KDA_KERNEL_GDR_PREP, s, [&] { return launch_gdr_prep(P, s); });
     if (e == cudaSuccess)
         e = timed_launch(KDA_KERNEL_GDR_BWD_CHAIN, s, [&] { return launch_gdr_bwd_chain(P, s); });
     if (e == cudaSuccess)

@@ -33,63 +33,6 @@ namespace {
 
 using namespace gdr;
 
-// ---- the largest incoming gradient of each (sequence, key head) ---------------------------
-constexpr int kAmaxThreads = 256;
-
-// one CTA per (chunk, key head): dO of the chunk's tokens and a share of the last state's gradient
-__global__ void __launch_bounds__(kAmaxThreads) gdr_amax_kernel(GdrBackward B) {
-    const GdrInputs& I = B.fwd.in;
-    int n, c;
-    if (!find_chunk(I, B.fwd.chunks, blockIdx.x, n, c)) return;
-    const int hk = blockIdx.y, share = I.Hv / I.Hk, tid = threadIdx.x;
-    const Span span = span_of(I, B.fwd.chunks, n);
-    const int rows = min(kC, span.len - c * kC), units = share * 16;   // 16-byte units of a token
-    const __nv_bfloat16* src = B.dout + ((span.start + (long long)c * kC) * I.Hv + hk * share) * kDim;
-    unsigned top = 0;
-    const auto take = [](unsigned u, unsigned& m) {   // two bf16 values; NaN compares above infinity
-        m = max(m, max(u & 0x7FFF0000u, (u & 0x7FFFu) << 16));
-    };
-    for (int at = tid & 31; at < units; at += 32) {
-#pragma unroll
-        for (int i = 0; i < kC; i += kAmaxThreads / 32) {
-            const int row = i + (tid >> 5);
-            uint4 u = make_uint4(0u, 0u, 0u, 0u);
-            if (row < rows) u = __ldg(reinterpret_cast<const uint4*>(src + (size_t)row * I.Hv * kDim + at * 8));
-            take(u.x, top); take(u.y, top); take(u.z, top); take(u.w, top);
-        }
-    }
-    top = __float_as_uint(fabsf(I.scale) * __uint_as_float(top));
-    unsigned dfinal_top = 0;
-    if (B.dfinal) {
-        const size_t base = ((size_t)n * I.Hv + hk * share) * kDim * kDim, count = (size_t)share * kDim * kDim;
-        const size_t first = (size_t)c * kAmaxThreads + tid, step = (size_t)((span.len + kC - 1) / kC) * kAmaxThreads;
-        const bool f32 = B.dfinal_dtype == KDA_F32;
-        const size_t per = f32 ? 4 : 8;        // values of 16 bytes
-        const uint4* p = reinterpret_cast<const uint4*>(static_cast<const unsigned char*>(B.dfinal) + base * (16 / per));
-        for (size_t i = first; i < count / per; i += 8 * step) {
-            uint4 u[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) u[j] = i + j * step < count / per ? __ldg(p + i + j * step) : make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                if (f32) {
-                    dfinal_top = max(dfinal_top, max(max(u[j].x & 0x7FFFFFFFu, u[j].y & 0x7FFFFFFFu), max(u[j].z & 0x7FFFFFFFu, u[j].w & 0x7FFFFFFFu)));
-                } else {
-                    take(u[j].x, dfinal_top); take(u[j].y, dfinal_top); take(u[j].z, dfinal_top); take(u[j].w, dfinal_top);
-                }
-            }
-        }
-    }
-    __shared__ unsigned s_top;
-    if (tid == 0) s_top = 0;
-    __syncthreads();
-    top = __reduce_max_sync(0xFFFFFFFFu, max(top, dfinal_top));
-    if ((tid & 31) == 0) atomicMax(&s_top, top);
-    __syncthreads();
-    // a maximum does not depend on the order of the atomics
-    if (tid == 0) atomicMax(&B.amax[(size_t)n * I.Hk + hk], s_top);
-}
-
 // ---- chunk by chunk ---------------------------------------------------------------------------
 // One CTA of 16 warps per (chunk, key head), which walks the group's value heads.  Warp w
 // forms rows (tokens) 16 (w & 3) .. of dQ and dK for the key channels 32 (w >> 2) .., and
@@ -213,7 +156,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) gdr_bwd_chunk_kernel(GdrBack
         const size_t at = (size_t)p.chunk * I.Hv + h;
         copy_tile(S.s, P.states + at * kStateTile, kStateTile, tid);
         copy_tile(S.y, B.ys + at * kTokenTile, kTokenTile, tid);
-        fetch_rows(S.o, B.dout + (p.tok * I.Hv + h) * kDim, (long long)I.Hv * kDim, p.rows, tid);
+        fetch_rows(S.o, B.in.dout + (p.tok * I.Hv + h) * kDim, (long long)I.Hv * kDim, p.rows, tid);
     };
     const auto fetch_second = [&](const Place& p, int h) {
         const size_t at = (size_t)p.chunk * I.Hv + h;
@@ -226,7 +169,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) gdr_bwd_chunk_kernel(GdrBack
         if (tid < 128) {                       // dO and V: lines of 64 channels
             const int row = tid >> 1, ch = 64 * (tid & 1);
             if (row < p.rows) {
-                asm volatile("prefetch.global.L2 [%0];\n" ::"l"(B.dout + ((p.tok + row) * I.Hv + h) * kDim + ch));
+                asm volatile("prefetch.global.L2 [%0];\n" ::"l"(B.in.dout + ((p.tok + row) * I.Hv + h) * kDim + ch));
                 asm volatile("prefetch.global.L2 [%0];\n" ::"l"(I.v + (p.tok + row) * I.v_stride + h * kDim + ch));
             }
         } else if (tid == 128) {
@@ -249,7 +192,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) gdr_bwd_chunk_kernel(GdrBack
     more = place(P, pair, next);
     const int hk = now.hk, rows = now.rows;
     const long long tok = now.tok;
-    const float sigma = grad_scale(B.amax[(size_t)now.n * I.Hk + hk]), back = 1.0f / sigma;
+    const float sigma = grad_scale(B.in.amax[(size_t)now.n * I.Hk + hk]), back = 1.0f / sigma;
     const uint32_t sk = smem_u32(S.k[kq]), sq = smem_u32(S.q[kq]);
 #pragma unroll
     for (int j = 0; j < 4; ++j)
@@ -560,12 +503,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1) gdr_bwd_chunk_kernel(GdrBack
 }
 
 }  // namespace
-
-cudaError_t launch_gdr_amax(const GdrBackward& B, cudaStream_t s) {
-    if (B.fwd.chunks.total == 0) return cudaSuccess;
-    gdr_amax_kernel<<<dim3(B.fwd.chunks.total, B.fwd.in.Hk), kAmaxThreads, 0, s>>>(B);
-    return cudaGetLastError();
-}
 
 cudaError_t launch_gdr_bwd_chunk(const GdrBackward& B, int sms, cudaStream_t s) {
     if (B.fwd.chunks.total == 0) return cudaSuccess;

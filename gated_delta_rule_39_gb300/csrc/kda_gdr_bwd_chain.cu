@@ -109,10 +109,10 @@ __device__ void back_queries(const GdrBackward& B, BackSmem& S, const Span& span
                         kGateE + row0 + 8 * (unit & 7);
     const size_t step = (size_t)I.Hv * (kBlockBytes / 4);
     const long long o_stride = (long long)I.Hv * kDim;
-    Rows q(I.q, I.q_stride, span, hk * kDim, p), o(B.dout, o_stride, span, h * kDim, p);
+    Rows q(I.q, I.q_stride, span, hk * kDim, p), o(B.in.dout, o_stride, span, h * kDim, p);
     const auto ahead = [&](int c) {
         prefetch_rows(I.q, I.q_stride, span, hk * kDim, c, p);
-        prefetch_rows(B.dout, o_stride, span, h * kDim, c, p);
+        prefetch_rows(B.in.dout, o_stride, span, h * kDim, c, p);
     };
     q.fetch(nch - 1);
     o.fetch(nch - 1);
@@ -197,7 +197,7 @@ __device__ void back_states(const GdrBackward& B, BackSmem& S, const Span& span,
     uint32_t x[2][32];
 #pragma unroll
     for (int i = 0; i < 64; ++i)
-        x[i >> 5][i & 31] = __float_as_uint(B.dfinal ? sigma * load_state(B.dfinal, B.dfinal_dtype, at + (size_t)i * kDim) : 0.0f);
+        x[i >> 5][i & 31] = __float_as_uint(B.in.dfinal ? sigma * load_state(B.in.dfinal, B.in.dfinal_dtype, at + (size_t)i * kDim) : 0.0f);
     for (int i = 0; i < nch; ++i) {
         const int c = nch - 1 - i;
         const unsigned turn = (unsigned)(i & 1);
@@ -279,7 +279,7 @@ __device__ __forceinline__ void back_run(const GdrBackward& B, BackSmem& S, int 
     const Span span = span_of(I, P.chunks, n);
     const int nch = (int)uniform((span.len + kC - 1) / kC);
     const int tid = threadIdx.x, lane = tid & 31, w = (int)uniform(tid >> 5);
-    const float sigma = grad_scale(B.amax[(size_t)n * I.Hk + h / (I.Hv / I.Hk)]);
+    const float sigma = grad_scale(B.in.amax[(size_t)n * I.Hk + h / (I.Hv / I.Hk)]);
     if (tid == 0) {
         for (int i = 0; i < kStages; ++i) {
             bar_init(&S.full[i], 2 * kProducers);

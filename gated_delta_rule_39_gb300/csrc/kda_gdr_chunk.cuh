@@ -192,12 +192,16 @@ struct GdrChunked {       // a chunked forward pass
     unsigned char* ts = nullptr;      // [chunk][Hv] of kTileBytes: T without beta
 };
 
-struct GdrBackward {      // what the backward pass has besides
-    GdrChunked fwd;
+struct GdrGrads {         // the gradients that enter a backward pass
     const __nv_bfloat16* dout;        // [tokens][Hv][128]
     const void* dfinal;               // [N][Hv][128][128] or nullptr
     int dfinal_dtype;
-    unsigned* amax;                   // [N][Hk]
+    unsigned* amax;                   // [N][Hk], 0 at first
+};
+
+struct GdrBackward {      // what the backward pass has besides
+    GdrChunked fwd;
+    GdrGrads in;
     unsigned char* dstates;           // [chunk][Hv] of kStateTile: gradient of the state after
     unsigned char* ys;                // [chunk][Hv] of kTokenTile: Y^T
     __nv_bfloat16 *dq, *dk, *dv;      // [tokens][heads][128]
@@ -206,11 +210,11 @@ struct GdrBackward {      // what the backward pass has besides
     int dinit_dtype;
 };
 
-cudaError_t launch_gdr_amax(const GdrBackward& P, cudaStream_t s);
 cudaError_t launch_gdr_bwd_chain(const GdrBackward& P, cudaStream_t s);
 cudaError_t launch_gdr_bwd_chunk(const GdrBackward& P, int sms, cudaStream_t s);
 cudaError_t launch_gdr_map(const GdrInputs& in, int* first, int* valid, int* err, cudaStream_t s);
 cudaError_t launch_gdr_prep(const GdrChunked& P, cudaStream_t s);
+cudaError_t launch_gdr_prep(const GdrBackward& P, cudaStream_t s);   // finds the largest gradients too
 cudaError_t launch_gdr_chain(const GdrChunked& P, cudaStream_t s);
 
 }  // namespace kda

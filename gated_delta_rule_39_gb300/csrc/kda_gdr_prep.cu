@@ -75,6 +75,7 @@ struct PrepSmem {
     };
     float g[kC];                                           // running sum of g in base 2
     float b[kC];
+    unsigned top[kPrepThreads / 32];
 };
 
 // rows [0, 64) of one head, zeros from row `rows` on, into a tile of 256-byte rows
@@ -137,7 +138,56 @@ __device__ __forceinline__ void put_negative(float (*M)[kLd], int row, int col, 
     }
 }
 
-__global__ void __launch_bounds__(kPrepThreads, 5) gdr_prep_kernel(GdrChunked P) {
+// Backward: the largest magnitude of the gradients that enter a (sequence, key head), by all its
+// chunks' CTAs: scale dO of the chunk's tokens and a share of the last state's gradient.
+__device__ __forceinline__ void largest_gradient(const GdrInputs& I, const GdrGrads& B, const Span& span, int n, int c, int hk,
+                                                 unsigned* shared_top, int tid) {
+    const int share = I.Hv / I.Hk, rows = min(kC, span.len - c * kC), units = share * 16;   // 16-byte units of a token
+    const __nv_bfloat16* src = B.dout + ((span.start + (long long)c * kC) * I.Hv + hk * share) * kDim;
+    const auto bits = [](unsigned u) {         // two bf16 values; NaN compares above infinity
+        return max(u & 0x7FFF0000u, (u & 0x7FFFu) << 16);
+    };
+    const auto four = [&](uint4 u) { return max(max(bits(u.x), bits(u.y)), max(bits(u.z), bits(u.w))); };
+    unsigned top = 0;
+    for (int at = tid & 31; at < units; at += 32) {
+#pragma unroll
+        for (int i = 0; i < kC; i += 8 * (kPrepThreads / 32)) {
+            uint4 u[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int row = i + j * (kPrepThreads / 32) + (tid >> 5);
+                u[j] = __ldg(reinterpret_cast<const uint4*>(src + (size_t)min(row, rows - 1) * I.Hv * kDim + at * 8));
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) top = max(top, four(u[j]));
+        }
+    }
+    top = __float_as_uint(fabsf(I.scale) * __uint_as_float(top));
+    if (B.dfinal) {
+        const bool f32 = B.dfinal_dtype == KDA_F32;
+        const size_t base = ((size_t)n * I.Hv + hk * share) * kDim * kDim, count = (size_t)share * kDim * kDim;
+        const size_t per = f32 ? 4 : 8;        // values of 16 bytes
+        const size_t step = (size_t)((span.len + kC - 1) / kC) * kPrepThreads;
+        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const unsigned char*>(B.dfinal) + base * (16 / per));
+        for (size_t i = (size_t)c * kPrepThreads + tid; i < count / per; i += 8 * step) {
+            uint4 u[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) u[j] = i + j * step < count / per ? __ldg(src + i + j * step) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                top = max(top, f32 ? max(max(u[j].x & 0x7FFFFFFFu, u[j].y & 0x7FFFFFFFu), max(u[j].z & 0x7FFFFFFFu, u[j].w & 0x7FFFFFFFu))
+                                   : four(u[j]));
+        }
+    }
+    top = __reduce_max_sync(0xFFFFFFFFu, top);
+    if ((tid & 31) == 0) shared_top[tid >> 5] = top;
+    __syncthreads();
+    // a maximum does not depend on the order of the atomics
+    if (tid == 0) atomicMax(&B.amax[(size_t)n * I.Hk + hk], max(max(shared_top[0], shared_top[1]), max(shared_top[2], shared_top[3])));
+}
+
+template <bool kGrads>
+__global__ void __launch_bounds__(kPrepThreads, 5) gdr_prep_kernel(GdrChunked P, GdrGrads B) {
     extern __shared__ __align__(128) unsigned char raw[];
     PrepSmem& S = *reinterpret_cast<PrepSmem*>(raw);
     const GdrInputs& I = P.in;
@@ -172,6 +222,7 @@ __global__ void __launch_bounds__(kPrepThreads, 5) gdr_prep_kernel(GdrChunked P)
         }
     };
     fetch_gates(hk * share);
+    if (kGrads) largest_gradient(I, B, span, n, c, hk, S.top, tid);
     cp_async_wait<0>();
     __syncthreads();
     // rows 16 w ..  of K K^T and Q K^T, columns 0 .. 16 w + 15
@@ -326,7 +377,7 @@ __global__ void __launch_bounds__(kPrepThreads, 5) gdr_prep_kernel(GdrChunked P)
             }
             const int at = row * 128 + ((unit ^ (row & 7)) << 4);
             *reinterpret_cast<uint4*>(block + at) = x;
-            if (P.ts)
+            if (kGrads)
                 *reinterpret_cast<uint4*>(P.ts + ((size_t)chunk * I.Hv + h) * kTileBytes + at) = y;
             *reinterpret_cast<uint4*>(block + kTileBytes + at) = *reinterpret_cast<const uint4*>(S.p + at);
         }
@@ -340,12 +391,16 @@ cudaError_t launch_gdr_map(const GdrInputs& in, int* first, int* valid, int* err
     return cudaGetLastError();
 }
 
-cudaError_t launch_gdr_prep(const GdrChunked& P, cudaStream_t s) {
+template <bool kGrads>
+static cudaError_t launch_prep(const GdrChunked& P, const GdrGrads& B, cudaStream_t s) {
     if (P.chunks.total == 0) return cudaSuccess;
-    const cudaError_t e = allow_smem<gdr_prep_kernel>(sizeof(PrepSmem));
+    const cudaError_t e = allow_smem<gdr_prep_kernel<kGrads>>(sizeof(PrepSmem));
     if (e != cudaSuccess) return e;
-    gdr_prep_kernel<<<dim3(P.chunks.total, P.in.Hk), kPrepThreads, sizeof(PrepSmem), s>>>(P);
+    gdr_prep_kernel<kGrads><<<dim3(P.chunks.total, P.in.Hk), kPrepThreads, sizeof(PrepSmem), s>>>(P, B);
     return cudaGetLastError();
 }
+
+cudaError_t launch_gdr_prep(const GdrChunked& P, cudaStream_t s) { return launch_prep<false>(P, {}, s); }
+cudaError_t launch_gdr_prep(const GdrBackward& B, cudaStream_t s) { return launch_prep<true>(B.fwd, B.in, s); }
 
 }  // namespace kda

@@ -527,10 +527,9 @@ enum {
     KDA_KERNEL_GDR_MAP = 14,
     KDA_KERNEL_GDR_PREP = 15,
     KDA_KERNEL_GDR_CHAIN = 16,
-    KDA_KERNEL_GDR_AMAX = 17,
-    KDA_KERNEL_GDR_BWD_CHAIN = 18,
-    KDA_KERNEL_GDR_BWD_CHUNK = 19,
-    KDA_NUM_KERNELS = 20
+    KDA_KERNEL_GDR_BWD_CHAIN = 17,
+    KDA_KERNEL_GDR_BWD_CHUNK = 18,
+    KDA_NUM_KERNELS = 19
 };
 int kda_profile_enable(int on);
 int kda_profile_read(double* total_ms, long long* launches);
