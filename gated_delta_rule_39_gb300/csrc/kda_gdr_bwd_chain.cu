@@ -89,7 +89,8 @@ __device__ void back_keys(const GdrBackward& B, BackSmem& S, const Span& span, i
             *reinterpret_cast<uint4*>(G.kb + dst + 1024 * j) = scaled_half8(k.x[j], -be);
         }
         tc::fence_proxy_async_smem();         // the MMAs read what was stored here
-        if (p < 32) bar_wait(&S.copied[st], phase, P.err);   // `full` means the copies too
+        // `full` means the copies too, and no copy is on its way when the warp that started it leaves
+        if (p < 32) bar_wait(&S.copied[st], phase, P.err, kDrainTries);
         bar_arrive(&S.full[st]);
         if (c > 0) {
             k.fetch(c - 1);
@@ -323,8 +324,8 @@ __device__ __forceinline__ void back_run(const GdrBackward& B, BackSmem& S, int 
         // every MMA and every arrival of this warp is over, and all other warps have left tensor
         // memory, before it is freed
         tc::commit_on(smem_u32(&S.drain), tc::elect());
-        bar_wait(&S.drain, 0u, P.err);
-        bar_wait(&S.done, 0u, P.err);
+        bar_wait(&S.drain, 0u, P.err, kDrainTries);
+        bar_wait(&S.done, 0u, P.err, kDrainTries);
         tc::fence_after_sync();
         tc::tmem_dealloc(tmem, kTmCols);
         return;

@@ -80,7 +80,7 @@ __device__ inline void keys(const GdrChunked& P, const CUtensorMap& vmap, ChainS
     // no copy is on its way when the warp that started it leaves
     const auto leave = [&](int begun) {
         if (p < 32)
-            for (int c = max(0, begun - kStages); c < begun; ++c) bar_wait(&S.copied[c % kStages], (unsigned)((c / kStages) & 1), P.err);
+            for (int c = max(0, begun - kStages); c < begun; ++c) bar_wait(&S.copied[c % kStages], (unsigned)((c / kStages) & 1), P.err, kDrainTries);
     };
     k.fetch(0);
     float ga = gate[0];
@@ -349,8 +349,8 @@ __device__ __forceinline__ void run(const GdrChunked& P, const CUtensorMap& vmap
         // every MMA and every arrival of this warp is over, and all other warps have left tensor
         // memory, before it is freed
         tc::commit_on(smem_u32(&S.drain), tc::elect());
-        bar_wait(&S.drain, 0u, P.err);
-        bar_wait(&S.done, 0u, P.err);
+        bar_wait(&S.drain, 0u, P.err, kDrainTries);
+        bar_wait(&S.done, 0u, P.err, kDrainTries);
         tc::fence_after_sync();
         tc::tmem_dealloc(tmem, kTmCols);
         return;

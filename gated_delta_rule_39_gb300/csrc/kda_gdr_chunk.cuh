@@ -74,18 +74,21 @@ __device__ __forceinline__ bool find_chunk(const GdrInputs& I, const Chunks& C, 
 }
 
 // ---- mbarriers ----------------------------------------------------------------------
+// Of a wait for what is on its way already (copies, MMAs, warps that are leaving): a role that
+// gave up on something else still waits for these.
+constexpr unsigned kDrainTries = 1u << 20;
 __device__ __forceinline__ void bar_init(uint64_t* b, int count) {
     asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;\n" ::"r"(smem_u32(b)), "r"(count));
 }
 __device__ __forceinline__ void bar_arrive(uint64_t* b) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(smem_u32(b)) : "memory");
 }
-// Waits, as a whole warp, for a phase to end; after KDA_WAIT_TRIES tries (each of which sleeps
+// Waits, as a whole warp, for a phase to end; after `tries` tries (each of which sleeps
 // for up to 20 us, as the hardware sees fit) records a timeout and gives up.  Every lane gets
 // the same answer.  Kept short: it is part of every role's loop.
-__device__ __forceinline__ bool bar_wait(uint64_t* b, unsigned parity, int* err) {
+__device__ __forceinline__ bool bar_wait(uint64_t* b, unsigned parity, int* err, unsigned tries = KDA_WAIT_TRIES) {
 #pragma unroll 1
-    for (unsigned n = 0; n < KDA_WAIT_TRIES; ++n) {
+    for (unsigned n = 0; n < tries; ++n) {
         unsigned ok;
         asm volatile(
             "{\n .reg .pred p;\n"
