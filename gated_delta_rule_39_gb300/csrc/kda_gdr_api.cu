@@ -56,11 +56,11 @@ bool states_clash(const void* s0, size_t n0, int d0, const void* s1, size_t n1, 
 }
 
 // Where a call's chunks are; returns the bytes of the map of packed sequences (first chunk
-// of each, and whether the offsets are valid).
+// of each, whether the offsets are valid, and the sequences by length).
 size_t plan_chunks(bool varlen, int B, int T, int N, gdr::Chunks* c) {
     c->per_seq = varlen ? 0 : (T + gdr::kC - 1) / gdr::kC;
     c->total = varlen ? T / gdr::kC + N : B * c->per_seq;
-    return varlen ? align_up(((size_t)N + 2) * sizeof(int)) : 0;
+    return varlen ? align_up((2 * (size_t)N + 2) * sizeof(int)) : 0;
 }
 
 // Scratch of a backward pass (bytes from its start): the map of packed sequences, the
@@ -180,8 +180,9 @@ int kda_gdr_fwd(const void* q, const void* k, const void* v, const void* g, cons
         int* first = reinterpret_cast<int*>(scratch);
         P.chunks.first = first;
         P.in.valid = first + N + 1;
+        P.chunks.order = first + N + 2;
         e = timed_launch(KDA_KERNEL_GDR_MAP, s,
-                         [&] { return launch_gdr_map(P.in, first, first + N + 1, P.err, s); });
+                         [&] { return launch_gdr_map(P.in, first, first + N + 2, first + N + 1, P.err, s); });
     }
     if (e == cudaSuccess) e = timed_launch(KDA_KERNEL_GDR_PREP, s, [&] { return launch_gdr_prep(P, s); });
     if (e == cudaSuccess)
@@ -269,8 +270,9 @@ int kda_gdr_bwd(const void* q, const void* k, const void* v, const void* g, cons
         int* first = reinterpret_cast<int*>(scratch);
         P.fwd.chunks.first = first;
         in.valid = first + N + 1;
+        P.fwd.chunks.order = first + N + 2;
         e = timed_launch(KDA_KERNEL_GDR_MAP, s,
-                         [&] { return launch_gdr_map(in, first, first + N + 1, P.fwd.err, s); });
+                         [&] { return launch_gdr_map(in, first, first + N + 2, first + N + 1, P.fwd.err, s); });
     }
     if (e == cudaSuccess) e = cudaMemsetAsync(P.in.amax, 0, (size_t)N * Hk * 4, s);
     if (e == cudaSuccess) e = timed_launch(KDA_KERNEL_GDR_PREP, s, [&] { return launch_gdr_prep(P, s); });

@@ -344,7 +344,7 @@ __global__ void __launch_bounds__(kBackThreads, 1) gdr_bwd_chain_kernel(GdrBackw
     extern __shared__ __align__(1024) unsigned char raw[];
     const GdrInputs& I = B.fwd.in;
     if (I.cu && !*I.valid) return;
-    const int units = gridDim.x / 2, unit = blockIdx.x % units, n = unit / I.Hv, h = unit % I.Hv;
+    const int units = gridDim.x / 2, unit = blockIdx.x % units, n = sequence_of(B.fwd.chunks, unit / I.Hv), h = unit % I.Hv;
     if (blockIdx.x < units) back_run(B, aligned_smem<BackSmem>(raw), n, h);
     else chain::run<true>(B.fwd, vmap, aligned_smem<chain::ChainSmem>(raw), n, h);
 }

@@ -9,7 +9,8 @@ using namespace gdr;
 __global__ void __launch_bounds__(chain::kChainThreads, 1) gdr_chain_kernel(GdrChunked P, const __grid_constant__ CUtensorMap vmap) {
     extern __shared__ __align__(1024) unsigned char raw[];
     if (P.in.cu && !*P.in.valid) return;
-    chain::run<false>(P, vmap, aligned_smem<chain::ChainSmem>(raw), blockIdx.x / P.in.Hv, blockIdx.x % P.in.Hv);
+    chain::run<false>(P, vmap, aligned_smem<chain::ChainSmem>(raw), sequence_of(P.chunks, blockIdx.x / P.in.Hv),
+                      blockIdx.x % P.in.Hv);
 }
 
 }  // namespace

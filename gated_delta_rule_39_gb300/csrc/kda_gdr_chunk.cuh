@@ -40,6 +40,7 @@ constexpr int kBlockBytes = (kBlockUsed + 127) / 128 * 128;
 
 struct Chunks {           // where the chunks of each sequence are
     const int* first;     // [N + 1] first chunk of each sequence (packed), or nullptr
+    const int* order;     // [N] the sequences by falling length (packed), or nullptr
     int per_seq;          // fixed length: chunks of each sequence
     int total;            // chunks in all (packed: an upper bound)
 };
@@ -53,6 +54,9 @@ __device__ __forceinline__ Span span_of(const GdrInputs& I, const Chunks& C, int
     if (I.cu) return {I.cu[n], I.cu[n + 1] - I.cu[n], C.first[n]};
     return {(long long)n * I.T, I.T, n * C.per_seq};
 }
+
+// The i-th sequence that a chain kernel takes.
+__device__ __forceinline__ int sequence_of(const Chunks& C, int i) { return C.order ? C.order[i] : i; }
 
 // Sequence and place of a chunk; false past the end of packed sequences (or for bad ones).
 __device__ __forceinline__ bool find_chunk(const GdrInputs& I, const Chunks& C, int chunk, int& n, int& c) {
@@ -215,7 +219,7 @@ struct GdrBackward {      // what the backward pass has besides
 
 cudaError_t launch_gdr_bwd_chain(const GdrBackward& P, cudaStream_t s);
 cudaError_t launch_gdr_bwd_chunk(const GdrBackward& P, int sms, cudaStream_t s);
-cudaError_t launch_gdr_map(const GdrInputs& in, int* first, int* valid, int* err, cudaStream_t s);
+cudaError_t launch_gdr_map(const GdrInputs& in, int* first, int* order, int* valid, int* err, cudaStream_t s);
 cudaError_t launch_gdr_prep(const GdrChunked& P, cudaStream_t s);
 cudaError_t launch_gdr_prep(const GdrBackward& P, cudaStream_t s);   // finds the largest gradients too
 cudaError_t launch_gdr_chain(const GdrChunked& P, cudaStream_t s);

@@ -8,14 +8,25 @@ namespace {
 
 using namespace gdr;
 
-// ---- map: checks cu_seqlens, first[n] = chunks of the sequences before n ------------------
+// ---- map: checks cu_seqlens, first[n] = chunks of the sequences before n, order = the sequences, long
+// ones first (so that the chains, a CTA per sequence and head, end together: 9 prompts of 1 to 18
+// chunks x 32 heads on 152 SMs take 11 us less) ----------------------------------------------
 constexpr int kMapThreads = 1024;
+constexpr int kBuckets = 128;             // of lengths: four to a factor of two
 
-__global__ void __launch_bounds__(kMapThreads) gdr_map_kernel(GdrInputs I, int* first, int* valid, int* err) {
+__device__ __forceinline__ int bucket_of(int chunks) {     // long sequences first
+    if (chunks < 4) return kBuckets - 1 - chunks;
+    const int e = 31 - __clz(chunks);
+    return kBuckets - 1 - (4 * (e - 1) + ((chunks >> (e - 2)) & 3));
+}
+
+__global__ void __launch_bounds__(kMapThreads) gdr_map_kernel(GdrInputs I, int* first, int* order, int* valid, int* err) {
     __shared__ int sums[kMapThreads / 32];
+    __shared__ int places[kBuckets];
     __shared__ int bad;
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
     if (tid == 0) bad = I.cu[0] != 0 || I.cu[I.N] != I.T;
+    if (tid < kBuckets) places[tid] = 0;
     __syncthreads();
     for (int n = tid; n < I.N; n += kMapThreads)
         if (I.cu[n + 1] < I.cu[n]) bad = 1;
@@ -43,10 +54,38 @@ __global__ void __launch_bounds__(kMapThreads) gdr_map_kernel(GdrInputs I, int* 
             if (i == w) x += all;
             all += sums[i];
         }
-        if (n < I.N) first[n] = before + x - c;
+        if (n < I.N) {
+            first[n] = before + x - c;
+            atomicAdd(&places[bucket_of(c)], 1);
+        }
         before += all;
     }
     if (tid == 0) first[I.N] = before;
+    __syncthreads();
+    if (w == 0) {                      // where each bucket begins
+        int count[kBuckets / 32], sum = 0;
+#pragma unroll
+        for (int i = 0; i < kBuckets / 32; ++i) {
+            count[i] = places[kBuckets / 32 * lane + i];
+            sum += count[i];
+        }
+        int x = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xFFFFFFFFu, x, o);
+            if (lane >= o) x += y;
+        }
+        x -= sum;
+#pragma unroll
+        for (int i = 0; i < kBuckets / 32; ++i) {
+            places[kBuckets / 32 * lane + i] = x;
+            x += count[i];
+        }
+    }
+    __syncthreads();
+    // within a bucket as it comes: only which CTA takes what depends on it
+    for (int n = tid; n < I.N; n += kMapThreads)
+        order[atomicAdd(&places[bucket_of((I.cu[n + 1] - I.cu[n] + kC - 1) / kC)], 1)] = n;
 }
 
 // ---- prep -------------------------------------------------------------------------------
@@ -386,8 +425,8 @@ __global__ void __launch_bounds__(kPrepThreads, 5) gdr_prep_kernel(GdrChunked P,
 
 }  // namespace
 
-cudaError_t launch_gdr_map(const GdrInputs& in, int* first, int* valid, int* err, cudaStream_t s) {
-    gdr_map_kernel<<<1, kMapThreads, 0, s>>>(in, first, valid, err);
+cudaError_t launch_gdr_map(const GdrInputs& in, int* first, int* order, int* valid, int* err, cudaStream_t s) {
+    gdr_map_kernel<<<1, kMapThreads, 0, s>>>(in, first, order, valid, err);
     return cudaGetLastError();
 }
 
