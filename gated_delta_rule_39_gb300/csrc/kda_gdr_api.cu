@@ -161,8 +161,8 @@ int kda_gdr_fwd(const void* q, const void* k, const void* v, const void* g, cons
         overlaps(out, n_out, cu_seqlens, ((size_t)N + 1) * 4) ||
         overlaps(final_state, n_so, cu_seqlens, ((size_t)N + 1) * 4))
         return KDA_ERR_ALIAS;
-    int dev = 0;
-    rc = device_setup(&dev, &P.err);
+    int dev = 0, sms = 0;
+    rc = device_setup(&dev, &P.err, &sms);
     if (rc != KDA_OK) return rc;
     P.out = static_cast<__nv_bfloat16*>(out);
     P.init_state = initial_state;
@@ -184,7 +184,7 @@ int kda_gdr_fwd(const void* q, const void* k, const void* v, const void* g, cons
         e = timed_launch(KDA_KERNEL_GDR_MAP, s,
                          [&] { return launch_gdr_map(P.in, first, first + N + 2, first + N + 1, P.err, s); });
     }
-    if (e == cudaSuccess) e = timed_launch(KDA_KERNEL_GDR_PREP, s, [&] { return launch_gdr_prep(P, s); });
+    if (e == cudaSuccess) e = timed_launch(KDA_KERNEL_GDR_PREP, s, [&] { return launch_gdr_prep(P, sms, s); });
     if (e == cudaSuccess)
         e = timed_launch(KDA_KERNEL_GDR_CHAIN, s, [&] { return launch_gdr_chain(P, s); });
     cudaFreeAsync(scratch, s);
@@ -275,7 +275,7 @@ int kda_gdr_bwd(const void* q, const void* k, const void* v, const void* g, cons
                          [&] { return launch_gdr_map(in, first, first + N + 2, first + N + 1, P.fwd.err, s); });
     }
     if (e == cudaSuccess) e = cudaMemsetAsync(P.in.amax, 0, (size_t)N * Hk * 4, s);
-    if (e == cudaSuccess) e = timed_launch(KDA_KERNEL_GDR_PREP, s, [&] { return launch_gdr_prep(P, s); });
+    if (e == cudaSuccess) e = timed_launch(KDA_KERNEL_GDR_PREP, s, [&] { return launch_gdr_prep(P, sms, s); });
     if (e == cudaSuccess)
         e = timed_launch(KDA_KERNEL_GDR_BWD_CHAIN, s, [&] { return launch_gdr_bwd_chain(P, s); });
     if (e == cudaSuccess)

@@ -26,6 +26,7 @@
 // fixed order.
 #include <algorithm>
 
+#include "kda_cluster.cuh"
 #include "kda_gdr_chunk.cuh"
 
 namespace kda {
@@ -38,7 +39,9 @@ using namespace gdr;
 // forms rows (tokens) 16 (w & 3) .. of dQ and dK for the key channels 32 (w >> 2) .., and
 // the columns 16 (w >> 2) .. of the token-by-token products.  The CTAs, one per SM, walk the
 // (chunk, key head) pairs with a stride; a head's tiles are fetched while the one before is worked on, each
-// as soon as its place is free (without that, waiting for them took 40 % of the time).
+// as soon as its place is free (without that, waiting for them took 40 % of the time).  With
+// fewer pairs than SMs (kSplit), a cluster shares a pair's value heads and adds dQ and dK up,
+// in the order of its CTAs.
 constexpr int kChunkThreads = 512, kParts = kChunkThreads / 128;
 
 constexpr int kPairBytes = kBlockUsed - kTileBytes;   // of a block, from P on
@@ -129,12 +132,21 @@ __device__ __forceinline__ bool place(const GdrChunked& P, int pair, Place& p) {
     return true;
 }
 
+// four floats of another CTA of the cluster, at the same place
+__device__ __forceinline__ float4 peer_float4(const float* p, int rank) {
+    float4 x;
+    asm volatile("{\n .reg .b32 a;\n mapa.shared::cluster.u32 a, %4, %5;\n ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [a];\n}\n"
+                 : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w) : "r"(smem_u32(p)), "r"(rank) : "memory");
+    return x;
+}
+
 __device__ __forceinline__ void store_gate(void* p, int dtype, size_t i, float x) {
     if (dtype == KDA_F32) static_cast<float*>(p)[i] = x;
     else static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(x);
 }
 
-__global__ void __launch_bounds__(kChunkThreads, 1) gdr_bwd_chunk_kernel(GdrBackward B) {
+template <bool kSplit>
+__global__ void __launch_bounds__(kChunkThreads, 1) gdr_bwd_chunk_kernel(GdrBackward B, int split) {
     extern __shared__ __align__(128) unsigned char raw[];
     ChunkSmem& S = *reinterpret_cast<ChunkSmem*>(raw);
     const GdrChunked& P = B.fwd;
@@ -180,325 +192,355 @@ __global__ void __launch_bounds__(kChunkThreads, 1) gdr_bwd_chunk_kernel(GdrBack
         }
     };
     Place now, next;
-    int pair = blockIdx.x, turn = 0, kq = 0;
+    const int rank = kSplit ? (int)cluster_rank() : 0;
+    int pair = kSplit ? blockIdx.x / split : blockIdx.x, turn = 0, kq = 0;
     if (!place(P, pair, now)) return;
     fetch_pair(now, 0);
-    fetch_gates(now, now.hk * share, 0);
-    fetch_first(now, now.hk * share);
-    fetch_second(now, now.hk * share);
+    fetch_gates(now, now.hk * share + rank, 0);
+    fetch_first(now, now.hk * share + rank);
+    fetch_second(now, now.hk * share + rank);
     float dq[4][4], dk[4][4], kk[2][4];
     for (bool more = true; more; now = next, kq ^= 1) {
-    pair += gridDim.x;
-    more = place(P, pair, next);
-    const int hk = now.hk, rows = now.rows;
-    const long long tok = now.tok;
-    const float sigma = grad_scale(B.in.amax[(size_t)now.n * I.Hk + hk]), back = 1.0f / sigma;
-    const uint32_t sk = smem_u32(S.k[kq]), sq = smem_u32(S.q[kq]);
+        pair += gridDim.x;
+        more = !kSplit && place(P, pair, next);
+        const int hk = now.hk, rows = now.rows;
+        const long long tok = now.tok;
+        const float sigma = grad_scale(B.in.amax[(size_t)now.n * I.Hk + hk]), back = 1.0f / sigma;
+        const uint32_t sk = smem_u32(S.k[kq]), sq = smem_u32(S.q[kq]);
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+        for (int j = 0; j < 4; ++j)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) dq[j][e] = dk[j][e] = 0.0f;
-    for (int h = hk * share; h < (hk + 1) * share; ++h, turn ^= 1) {
-        const bool last = h + 1 == (hk + 1) * share;
-        const Place& then = last ? next : now;             // where the head after this one is
-        const int then_h = last ? next.hk * share : h + 1;
-        const bool follows = !last || more;
-        const unsigned char* pg = S.pg[turn];
-        const float* gate = reinterpret_cast<const float*>(pg + kTileBytes);
-        // values for Y.V: rows i0 and i1, a quarter of the channels
-        uint32_t v[2][4];
-        const __nv_bfloat16* vp = I.v + (tok + i0) * I.v_stride + h * kDim + 32 * part + 2 * t;
+            for (int e = 0; e < 4; ++e) dq[j][e] = dk[j][e] = 0.0f;
+        const int h0 = hk * share + rank, step = kSplit ? split : 1;
+        for (int h = h0; h < (hk + 1) * share; h += step, turn ^= 1) {
+            const bool last = h + step >= (hk + 1) * share;
+            const Place& then = last ? next : now;             // where the head after this one is
+            const int then_h = last ? next.hk * share : h + step;
+            const bool follows = !last || more;
+            const unsigned char* pg = S.pg[turn];
+            const float* gate = reinterpret_cast<const float*>(pg + kTileBytes);
+            // values for Y.V: rows i0 and i1, a quarter of the channels
+            uint32_t v[2][4];
+            const __nv_bfloat16* vp = I.v + (tok + i0) * I.v_stride + h * kDim + 32 * part + 2 * t;
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+            for (int i = 0; i < 2; ++i)
 #pragma unroll
-            for (int m = 0; m < 4; ++m)
-                v[i][m] = (m & 1 ? i1 : i0) < rows ? __ldg(reinterpret_cast<const uint32_t*>(vp + (m & 1 ? 8 * I.v_stride : 0) + 16 * i + 8 * (m >> 1))) : 0u;
-        asm volatile("cp.async.wait_all;\n" ::: "memory");
-        rows_to_half(S.o, I.scale * sigma, tid);
-        if (h == hk * share) {
-            rows_to_half(S.k[kq], 1.0f, tid);
-            rows_to_half(S.q[kq], 1.0f, tid);
-        }
-        __syncthreads();
-        if (follows) {
-            prefetch(then, then_h);
-            fetch_gates(then, then_h, turn ^ 1);
-            if (last) fetch_pair(next, kq ^ 1);
-        }
-        if (h == hk * share) {         // K K^T, this warp's 16 rows and 16 columns
-#pragma unroll
-            for (int j = 0; j < 2; ++j) kk[j][0] = kk[j][1] = kk[j][2] = kk[j][3] = 0.0f;
-#pragma unroll
-            for (int ks = 0; ks < 8; ++ks) {
-                uint32_t a[4], b[4];
-                ldsm(a, a_addr<256>(sk, 16 * rw, 2 * ks, lane));
-                ldsm(b, b_addr<256>(sk, 16 * part, 2 * ks, lane));
-                mma_f16(kk[0], a, b[0], b[1]);
-                mma_f16(kk[1], a, b[2], b[3]);
+                for (int m = 0; m < 4; ++m)
+                    v[i][m] = (m & 1 ? i1 : i0) < rows ? __ldg(reinterpret_cast<const uint32_t*>(vp + (m & 1 ? 8 * I.v_stride : 0) + 16 * i + 8 * (m >> 1))) : 0u;
+            asm volatile("cp.async.wait_all;\n" ::: "memory");
+            rows_to_half(S.o, I.scale * sigma, tid);
+            if (h == h0) {
+                rows_to_half(S.k[kq], 1.0f, tid);
+                rows_to_half(S.q[kq], 1.0f, tid);
             }
-        }
-        const float e0 = gate[kGateE + i0], e1 = gate[kGateE + i1];
-        const float be0 = gate[kGateBe + i0], be1 = gate[kGateBe + i1];
-        const float b0 = gate[kGateB + i0], b1 = gate[kGateB + i1];
-        {
-            float yv0 = 0.0f, yv1 = 0.0f;
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                uint32_t fy[4];
-                ldsm_t(fy, row_b(sy, 32 * part + 16 * i, 2 * rw, lane));
-#pragma unroll
-                for (int m = 0; m < 4; ++m) {              // rows i0, i1; channels 2 t (+ 8)
-                    const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&fy[m]));
-                    (m & 1 ? yv1 : yv0) += y.x * bf16_lo(v[i][m]) + y.y * bf16_hi(v[i][m]);
-                }
+            __syncthreads();
+            if (follows) {
+                prefetch(then, then_h);
+                fetch_gates(then, then_h, turn ^ 1);
+                if (last) fetch_pair(next, kq ^ 1);
             }
-            yv0 = quad_sum(yv0);
-            yv1 = quad_sum(yv1);
-            if (t == 0) {
-                S.yv[part][i0] = yv0; S.yv[part][i1] = yv1;
-            }
-        }
-        // <S, dS>: the diagonal of S^T dS, rows 16 (w / 2) .. over half of the key channels
-        {
-            float d[2][4] = {};
+            if (h == h0) {         // K K^T, this warp's 16 rows and 16 columns
 #pragma unroll
-            for (int ks = 0; ks < 4; ++ks) {
-                uint32_t a[4], b[4];
-                ldsm(a, row_a(ss, 16 * (w >> 1), 8 * (w & 1) + 2 * ks, lane));
-                ldsm(b, row_b(sds, 16 * (w >> 1), 8 * (w & 1) + 2 * ks, lane));
-                mma_f16(d[0], a, b[0], b[1]);
-                mma_f16(d[1], a, b[2], b[3]);
-            }
-            // rows g (and g + 8), columns 2 t, 2 t + 1 (and the same + 8)
-            float x = g == 2 * t ? d[0][0] + d[1][2] : g == 2 * t + 1 ? d[0][1] + d[1][3] : 0.0f;
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, o);
-            if (lane == 0) S.dot[w] = x;
-        }
-        {
-            // dO X^T and Y X^T: this warp's 16 rows, 16 columns
-            float dp[2][4], da[2][4];
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) dp[j][e] = da[j][e] = 0.0f;
-            if (part <= rw) {              // else columns past the rows
+                for (int j = 0; j < 2; ++j) kk[j][0] = kk[j][1] = kk[j][2] = kk[j][3] = 0.0f;
 #pragma unroll
                 for (int ks = 0; ks < 8; ++ks) {
-                    uint32_t fo[4], fy[4], b[4];
-                    ldsm(fo, a_addr<256>(so, 16 * rw, 2 * ks, lane));
-                    ldsm_t(fy, row_b(sy, 16 * ks, 2 * rw, lane));
-                    ldsm_t(b, row_a(sx, 16 * ks, 2 * part, lane));
-                    mma_f16(dp[0], fo, b[0], b[1]);
-                    mma_f16(dp[1], fo, b[2], b[3]);
-                    mma_f16(da[0], fy, b[0], b[1]);
-                    mma_f16(da[1], fy, b[2], b[3]);
+                    uint32_t a[4], b[4];
+                    ldsm(a, a_addr<256>(sk, 16 * rw, 2 * ks, lane));
+                    ldsm(b, b_addr<256>(sk, 16 * part, 2 * ks, lane));
+                    mma_f16(kk[0], a, b[0], b[1]);
+                    mma_f16(kk[1], a, b[2], b[3]);
                 }
             }
-            // dP, dB and the sums of dP . Q K^T + dB . K K^T (M . Q K^T is P)
-            uint32_t fp[2][2], fb[2][2];
-            float rs0 = 0.0f, rs1 = 0.0f, bs0 = 0.0f, bs1 = 0.0f;
+            const float e0 = gate[kGateE + i0], e1 = gate[kGateE + i1];
+            const float be0 = gate[kGateBe + i0], be1 = gate[kGateBe + i1];
+            const float b0 = gate[kGateB + i0], b1 = gate[kGateB + i1];
             {
-                const float g0 = gate[kGateG + i0], g1 = gate[kGateG + i1];
+                float yv0 = 0.0f, yv1 = 0.0f;
 #pragma unroll
-                for (int nt = 0; nt < 2; ++nt) {
-                    const int j = 16 * part + 8 * nt + 2 * t;
-                    float cs[2] = {0.0f, 0.0f}, pv[4], bv[4];
-                    const float2 gj = *reinterpret_cast<const float2*>(gate + kGateG + j);
+                for (int i = 0; i < 2; ++i) {
+                    uint32_t fy[4];
+                    ldsm_t(fy, row_b(sy, 32 * part + 16 * i, 2 * rw, lane));
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int i = e < 2 ? i0 : i1, jj = j + (e & 1);
-                        const float m = jj <= i ? ex2_approx((e < 2 ? g0 : g1) - (e & 1 ? gj.y : gj.x)) : 0.0f;
-                        const float pq = __half2float(*reinterpret_cast<const __half*>(
-                            pg + i * 128 + (((jj >> 3) ^ (i & 7)) << 4) + (jj & 7) * 2));
-                        const float mk = jj < i ? m * kk[nt][e] : 0.0f;
-                        const float dpv = dp[nt][e], dav = -da[nt][e], bi = e < 2 ? b0 : b1;
-                        pv[e] = jj <= i ? m * dpv : 0.0f;
-                        bv[e] = jj < i ? bi * m * dav : 0.0f;
-                        const float sum = (jj <= i ? dpv * pq : 0.0f) + bi * dav * mk;
-                        cs[e & 1] += sum;
-                        (e < 2 ? rs0 : rs1) += sum;
-                        (e < 2 ? bs0 : bs1) += dav * mk;
-                    }
-                    fp[nt][0] = pack_half2(pv[0], pv[1]);
-                    fp[nt][1] = pack_half2(pv[2], pv[3]);
-                    fb[nt][0] = pack_half2(bv[0], bv[1]);
-                    fb[nt][1] = pack_half2(bv[2], bv[3]);
-                    cs[0] = rows_sum(cs[0]);
-                    cs[1] = rows_sum(cs[1]);
-                    if (g == 0) {
-                        S.col[rw][j] = cs[0];
-                        S.col[rw][j + 1] = cs[1];
+                    for (int m = 0; m < 4; ++m) {              // rows i0, i1; channels 2 t (+ 8)
+                        const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&fy[m]));
+                        (m & 1 ? yv1 : yv0) += y.x * bf16_lo(v[i][m]) + y.y * bf16_hi(v[i][m]);
                     }
                 }
-                rs0 = quad_sum(rs0); rs1 = quad_sum(rs1); bs0 = quad_sum(bs0); bs1 = quad_sum(bs1);
+                yv0 = quad_sum(yv0);
+                yv1 = quad_sum(yv1);
                 if (t == 0) {
-                    S.row[3][part][i0] = rs0; S.row[3][part][i1] = rs1;
-                    S.row[4][part][i0] = bs0; S.row[4][part][i1] = bs1;
+                    S.yv[part][i0] = yv0; S.yv[part][i1] = yv1;
                 }
             }
-            stsm(a_addr<128>(sdp, 16 * rw, 2 * part, lane), fp[0][0], fp[0][1], fp[1][0], fp[1][1]);
-            stsm(a_addr<128>(sdb, 16 * rw, 2 * part, lane), fb[0][0], fb[0][1], fb[1][0], fb[1][1]);
-        }
-        // dO S^T and Y S^T: this warp's rows, 32 key channels, over 128 value channels
-        {
-            float a[4][4], z[4][4];
+            // <S, dS>: the diagonal of S^T dS, rows 16 (w / 2) .. over half of the key channels
+            {
+                float d[2][4] = {};
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
+                for (int ks = 0; ks < 4; ++ks) {
+                    uint32_t a[4], b[4];
+                    ldsm(a, row_a(ss, 16 * (w >> 1), 8 * (w & 1) + 2 * ks, lane));
+                    ldsm(b, row_b(sds, 16 * (w >> 1), 8 * (w & 1) + 2 * ks, lane));
+                    mma_f16(d[0], a, b[0], b[1]);
+                    mma_f16(d[1], a, b[2], b[3]);
+                }
+                // rows g (and g + 8), columns 2 t, 2 t + 1 (and the same + 8)
+                float x = g == 2 * t ? d[0][0] + d[1][2] : g == 2 * t + 1 ? d[0][1] + d[1][3] : 0.0f;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) a[j][e] = z[j][e] = 0.0f;
+                for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, o);
+                if (lane == 0) S.dot[w] = x;
+            }
+            {
+                // dO X^T and Y X^T: this warp's 16 rows, 16 columns
+                float dp[2][4], da[2][4];
 #pragma unroll
-            for (int ks = 0; ks < 8; ++ks) {
-                uint32_t fo[4], fy[4];
-                ldsm(fo, a_addr<256>(so, 16 * rw, 2 * ks, lane));
-                ldsm_t(fy, row_b(sy, 16 * ks, 2 * rw, lane));   // Y as an A operand from Y^T
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) dp[j][e] = da[j][e] = 0.0f;
+                if (part <= rw) {              // else columns past the rows
+#pragma unroll
+                    for (int ks = 0; ks < 8; ++ks) {
+                        uint32_t fo[4], fy[4], b[4];
+                        ldsm(fo, a_addr<256>(so, 16 * rw, 2 * ks, lane));
+                        ldsm_t(fy, row_b(sy, 16 * ks, 2 * rw, lane));
+                        ldsm_t(b, row_a(sx, 16 * ks, 2 * part, lane));
+                        mma_f16(dp[0], fo, b[0], b[1]);
+                        mma_f16(dp[1], fo, b[2], b[3]);
+                        mma_f16(da[0], fy, b[0], b[1]);
+                        mma_f16(da[1], fy, b[2], b[3]);
+                    }
+                }
+                // dP, dB and the sums of dP . Q K^T + dB . K K^T (M . Q K^T is P)
+                uint32_t fp[2][2], fb[2][2];
+                float rs0 = 0.0f, rs1 = 0.0f, bs0 = 0.0f, bs1 = 0.0f;
+                {
+                    const float g0 = gate[kGateG + i0], g1 = gate[kGateG + i1];
+#pragma unroll
+                    for (int nt = 0; nt < 2; ++nt) {
+                        const int j = 16 * part + 8 * nt + 2 * t;
+                        float cs[2] = {0.0f, 0.0f}, pv[4], bv[4];
+                        const float2 gj = *reinterpret_cast<const float2*>(gate + kGateG + j);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int i = e < 2 ? i0 : i1, jj = j + (e & 1);
+                            const float m = jj <= i ? ex2_approx((e < 2 ? g0 : g1) - (e & 1 ? gj.y : gj.x)) : 0.0f;
+                            const float pq = __half2float(*reinterpret_cast<const __half*>(
+                                pg + i * 128 + (((jj >> 3) ^ (i & 7)) << 4) + (jj & 7) * 2));
+                            const float mk = jj < i ? m * kk[nt][e] : 0.0f;
+                            const float dpv = dp[nt][e], dav = -da[nt][e], bi = e < 2 ? b0 : b1;
+                            pv[e] = jj <= i ? m * dpv : 0.0f;
+                            bv[e] = jj < i ? bi * m * dav : 0.0f;
+                            const float sum = (jj <= i ? dpv * pq : 0.0f) + bi * dav * mk;
+                            cs[e & 1] += sum;
+                            (e < 2 ? rs0 : rs1) += sum;
+                            (e < 2 ? bs0 : bs1) += dav * mk;
+                        }
+                        fp[nt][0] = pack_half2(pv[0], pv[1]);
+                        fp[nt][1] = pack_half2(pv[2], pv[3]);
+                        fb[nt][0] = pack_half2(bv[0], bv[1]);
+                        fb[nt][1] = pack_half2(bv[2], bv[3]);
+                        cs[0] = rows_sum(cs[0]);
+                        cs[1] = rows_sum(cs[1]);
+                        if (g == 0) {
+                            S.col[rw][j] = cs[0];
+                            S.col[rw][j + 1] = cs[1];
+                        }
+                    }
+                    rs0 = quad_sum(rs0); rs1 = quad_sum(rs1); bs0 = quad_sum(bs0); bs1 = quad_sum(bs1);
+                    if (t == 0) {
+                        S.row[3][part][i0] = rs0; S.row[3][part][i1] = rs1;
+                        S.row[4][part][i0] = bs0; S.row[4][part][i1] = bs1;
+                    }
+                }
+                stsm(a_addr<128>(sdp, 16 * rw, 2 * part, lane), fp[0][0], fp[0][1], fp[1][0], fp[1][1]);
+                stsm(a_addr<128>(sdb, 16 * rw, 2 * part, lane), fb[0][0], fb[0][1], fb[1][0], fb[1][1]);
+            }
+            // dO S^T and Y S^T: this warp's rows, 32 key channels, over 128 value channels
+            {
+                float a[4][4], z[4][4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) a[j][e] = z[j][e] = 0.0f;
+#pragma unroll
+                for (int ks = 0; ks < 8; ++ks) {
+                    uint32_t fo[4], fy[4];
+                    ldsm(fo, a_addr<256>(so, 16 * rw, 2 * ks, lane));
+                    ldsm_t(fy, row_b(sy, 16 * ks, 2 * rw, lane));   // Y as an A operand from Y^T
+#pragma unroll
+                    for (int np = 0; np < 2; ++np) {
+                        uint32_t b[4];
+                        ldsm_t(b, row_a(ss, 16 * ks, 4 * part + 2 * np, lane));
+                        mma_f16(a[2 * np], fo, b[0], b[1]);
+                        mma_f16(a[2 * np + 1], fo, b[2], b[3]);
+                        mma_f16(z[2 * np], fy, b[0], b[1]);
+                        mma_f16(z[2 * np + 1], fy, b[2], b[3]);
+                    }
+                }
+                float qa0 = 0.0f, qa1 = 0.0f, kz0 = 0.0f, kz1 = 0.0f;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int ch = 32 * part + 8 * j + 2 * t;
+                    const float2 q0 = half2_at(S.q[kq], i0, ch), q1 = half2_at(S.q[kq], i1, ch);
+                    const float2 k0 = half2_at(S.k[kq], i0, ch), k1 = half2_at(S.k[kq], i1, ch);
+                    a[j][0] *= e0; a[j][1] *= e0; a[j][2] *= e1; a[j][3] *= e1;
+                    qa0 += q0.x * a[j][0] + q0.y * a[j][1];
+                    qa1 += q1.x * a[j][2] + q1.y * a[j][3];
+                    kz0 += k0.x * z[j][0] + k0.y * z[j][1];
+                    kz1 += k1.x * z[j][2] + k1.y * z[j][3];
+                    dq[j][0] += a[j][0]; dq[j][1] += a[j][1]; dq[j][2] += a[j][2]; dq[j][3] += a[j][3];
+                    dk[j][0] -= be0 * z[j][0]; dk[j][1] -= be0 * z[j][1];
+                    dk[j][2] -= be1 * z[j][2]; dk[j][3] -= be1 * z[j][3];
+                }
+                qa0 = quad_sum(qa0); qa1 = quad_sum(qa1); kz0 = quad_sum(kz0); kz1 = quad_sum(kz1);
+                if (t == 0) {
+                    S.row[0][part][i0] = qa0; S.row[0][part][i1] = qa1;
+                    S.row[1][part][i0] = kz0; S.row[1][part][i1] = kz1;
+                }
+            }
+            __syncthreads();               // dP and dB are there; S, Y and dO have been read
+            if (follows) fetch_first(then, then_h);
+            // X dS^T
+            {
+                float a[4][4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) a[j][0] = a[j][1] = a[j][2] = a[j][3] = 0.0f;
+#pragma unroll
+                for (int ks = 0; ks < 8; ++ks) {
+                    uint32_t fx[4];
+                    ldsm_t(fx, row_b(sx, 16 * ks, 2 * rw, lane));
+#pragma unroll
+                    for (int np = 0; np < 2; ++np) {
+                        uint32_t b[4];
+                        ldsm_t(b, row_a(sds, 16 * ks, 4 * part + 2 * np, lane));
+                        mma_f16(a[2 * np], fx, b[0], b[1]);
+                        mma_f16(a[2 * np + 1], fx, b[2], b[3]);
+                    }
+                }
+                const float f0 = gate[kGateEnd + i0], f1 = gate[kGateEnd + i1];
+                float ka0 = 0.0f, ka1 = 0.0f;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int ch = 32 * part + 8 * j + 2 * t;
+                    const float2 k0 = half2_at(S.k[kq], i0, ch), k1 = half2_at(S.k[kq], i1, ch);
+                    a[j][0] *= f0; a[j][1] *= f0; a[j][2] *= f1; a[j][3] *= f1;
+                    ka0 += k0.x * a[j][0] + k0.y * a[j][1];
+                    ka1 += k1.x * a[j][2] + k1.y * a[j][3];
+                    dk[j][0] += a[j][0]; dk[j][1] += a[j][1]; dk[j][2] += a[j][2]; dk[j][3] += a[j][3];
+                }
+                ka0 = quad_sum(ka0); ka1 = quad_sum(ka1);
+                if (t == 0) {
+                    S.row[2][part][i0] = ka0; S.row[2][part][i1] = ka1;
+                }
+            }
+            __syncthreads();               // dS and X have been read, all sums are there
+            if (follows) fetch_second(then, then_h);
+            // dQ += dP K, dK += dP^T Q + dB K + dB^T K
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks) {
+                uint32_t fpn[4], fbn[4], fpt[4], fbt[4];
+                if (ks <= rw) {            // rows reach tokens up to their own
+                    ldsm(fpn, a_addr<128>(sdp, 16 * rw, 2 * ks, lane));
+                    ldsm(fbn, a_addr<128>(sdb, 16 * rw, 2 * ks, lane));
+                }
+                if (ks >= rw) {            // transposed: from their own on
+                    ldsm_t(fpt, b_addr<128>(sdp, 16 * ks, 2 * rw, lane));
+                    ldsm_t(fbt, b_addr<128>(sdb, 16 * ks, 2 * rw, lane));
+                }
 #pragma unroll
                 for (int np = 0; np < 2; ++np) {
                     uint32_t b[4];
-                    ldsm_t(b, row_a(ss, 16 * ks, 4 * part + 2 * np, lane));
-                    mma_f16(a[2 * np], fo, b[0], b[1]);
-                    mma_f16(a[2 * np + 1], fo, b[2], b[3]);
-                    mma_f16(z[2 * np], fy, b[0], b[1]);
-                    mma_f16(z[2 * np + 1], fy, b[2], b[3]);
+                    ldsm_t(b, a_addr<256>(sk, 16 * ks, 4 * part + 2 * np, lane));
+                    if (ks <= rw) {
+                        mma_f16(dq[2 * np], fpn, b[0], b[1]);
+                        mma_f16(dq[2 * np + 1], fpn, b[2], b[3]);
+                        mma_f16(dk[2 * np], fbn, b[0], b[1]);
+                        mma_f16(dk[2 * np + 1], fbn, b[2], b[3]);
+                    }
+                    if (ks >= rw) {
+                        mma_f16(dk[2 * np], fbt, b[0], b[1]);
+                        mma_f16(dk[2 * np + 1], fbt, b[2], b[3]);
+                        ldsm_t(b, a_addr<256>(sq, 16 * ks, 4 * part + 2 * np, lane));
+                        mma_f16(dk[2 * np], fpt, b[0], b[1]);
+                        mma_f16(dk[2 * np + 1], fpt, b[2], b[3]);
+                    }
                 }
             }
-            float qa0 = 0.0f, qa1 = 0.0f, kz0 = 0.0f, kz1 = 0.0f;
+            // gates: two tokens per lane of one warp
+            if (w == 0) {
+                float dgv[2], ka[2];
+#pragma unroll
+                for (int m = 0; m < 2; ++m) {
+                    const int j = 2 * lane + m;
+                    const auto parts = [&](const float (&x)[kParts][kC]) { return (x[0][j] + x[1][j]) + (x[2][j] + x[3][j]); };
+                    const float qa = parts(S.row[0]), kz = parts(S.row[1]), rs = parts(S.row[3]), bs = parts(S.row[4]), yv = parts(S.yv);
+                    ka[m] = parts(S.row[2]);
+                    const float cs = S.col[0][j] + S.col[1][j] + S.col[2][j] + S.col[3][j];
+                    dgv[m] = qa - ka[m] - gate[kGateBe + j] * kz + rs - cs;
+                    if (j < rows)
+                        store_gate(B.dbeta, I.gate_dtype, (size_t)(tok + j) * I.Hv + h,
+                                   back * (yv - gate[kGateE + j] * kz + bs));
+                }
+                float all = ka[0] + ka[1];
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xFFFFFFFFu, all, o);
+                float dot = 0.0f;
+#pragma unroll
+                for (int i = 0; i < kChunkThreads / 32; ++i) dot += S.dot[i];
+                if (lane == 31) dgv[1] += all + gate[kGateAll] * dot;
+                float x = dgv[0] + dgv[1];         // sums from a token to the chunk's last
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const float y = __shfl_down_sync(0xFFFFFFFFu, x, o);
+                    if (lane + o < 32) x += y;
+                }
+                if (2 * lane < rows) store_gate(B.dg, I.gate_dtype, (size_t)(tok + 2 * lane) * I.Hv + h, back * x);
+                if (2 * lane + 1 < rows)
+                    store_gate(B.dg, I.gate_dtype, (size_t)(tok + 2 * lane + 1) * I.Hv + h, back * (x - dgv[0]));
+            }
+        }
+        if constexpr (kSplit) {            // in place of S and dS: fp32 rows, 8-channel groups turned by the row
+            float* mine[2] = {reinterpret_cast<float*>(S.s), reinterpret_cast<float*>(S.ds)};
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int ch = 32 * part + 8 * j + 2 * t;
-                const float2 q0 = half2_at(S.q[kq], i0, ch), q1 = half2_at(S.q[kq], i1, ch);
-                const float2 k0 = half2_at(S.k[kq], i0, ch), k1 = half2_at(S.k[kq], i1, ch);
-                a[j][0] *= e0; a[j][1] *= e0; a[j][2] *= e1; a[j][3] *= e1;
-                qa0 += q0.x * a[j][0] + q0.y * a[j][1];
-                qa1 += q1.x * a[j][2] + q1.y * a[j][3];
-                kz0 += k0.x * z[j][0] + k0.y * z[j][1];
-                kz1 += k1.x * z[j][2] + k1.y * z[j][3];
-                dq[j][0] += a[j][0]; dq[j][1] += a[j][1]; dq[j][2] += a[j][2]; dq[j][3] += a[j][3];
-                dk[j][0] -= be0 * z[j][0]; dk[j][1] -= be0 * z[j][1];
-                dk[j][2] -= be1 * z[j][2]; dk[j][3] -= be1 * z[j][3];
+                const int at0 = i0 * kDim + (ch ^ (8 * (i0 & 7))), at1 = i1 * kDim + (ch ^ (8 * (i1 & 7)));
+                *reinterpret_cast<float2*>(mine[0] + at0) = make_float2(dq[j][0], dq[j][1]);
+                *reinterpret_cast<float2*>(mine[0] + at1) = make_float2(dq[j][2], dq[j][3]);
+                *reinterpret_cast<float2*>(mine[1] + at0) = make_float2(dk[j][0], dk[j][1]);
+                *reinterpret_cast<float2*>(mine[1] + at1) = make_float2(dk[j][2], dk[j][3]);
             }
-            qa0 = quad_sum(qa0); qa1 = quad_sum(qa1); kz0 = quad_sum(kz0); kz1 = quad_sum(kz1);
-            if (t == 0) {
-                S.row[0][part][i0] = qa0; S.row[0][part][i1] = qa1;
-                S.row[1][part][i0] = kz0; S.row[1][part][i1] = kz1;
-            }
-        }
-        __syncthreads();               // dP and dB are there; S, Y and dO have been read
-        if (follows) fetch_first(then, then_h);
-        // X dS^T
-        {
-            float a[4][4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) a[j][0] = a[j][1] = a[j][2] = a[j][3] = 0.0f;
-#pragma unroll
-            for (int ks = 0; ks < 8; ++ks) {
-                uint32_t fx[4];
-                ldsm_t(fx, row_b(sx, 16 * ks, 2 * rw, lane));
-#pragma unroll
-                for (int np = 0; np < 2; ++np) {
-                    uint32_t b[4];
-                    ldsm_t(b, row_a(sds, 16 * ks, 4 * part + 2 * np, lane));
-                    mma_f16(a[2 * np], fx, b[0], b[1]);
-                    mma_f16(a[2 * np + 1], fx, b[2], b[3]);
+            cluster_arrive();
+            cluster_wait();
+            // four channels of a row at a time, the rows between the CTAs
+            for (int i = rank * kChunkThreads + tid; i < 2 * kC * (kDim / 4); i += split * kChunkThreads) {
+                const int side = i / (kC * (kDim / 4)), row = i / (kDim / 4) % kC, ch = i % (kDim / 4) * 4;
+                float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                for (int r = 0; r < split; ++r) {
+                    const float4 x = peer_float4(mine[side] + row * kDim + (ch ^ (8 * (row & 7))), r);
+                    sum.x += x.x; sum.y += x.y; sum.z += x.z; sum.w += x.w;
                 }
+                if (row < rows)
+                    *reinterpret_cast<uint2*>((side ? B.dk : B.dq) + ((size_t)(tok + row) * I.Hk + hk) * kDim + ch) =
+                        make_uint2(pack_bf16(back * sum.x, back * sum.y), pack_bf16(back * sum.z, back * sum.w));
             }
-            const float f0 = gate[kGateEnd + i0], f1 = gate[kGateEnd + i1];
-            float ka0 = 0.0f, ka1 = 0.0f;
+            cluster_arrive();                  // until then the others read this CTA's part
+            cluster_wait();
+        } else {                               // dQ and dK as bf16 rows
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int ch = 32 * part + 8 * j + 2 * t;
-                const float2 k0 = half2_at(S.k[kq], i0, ch), k1 = half2_at(S.k[kq], i1, ch);
-                a[j][0] *= f0; a[j][1] *= f0; a[j][2] *= f1; a[j][3] *= f1;
-                ka0 += k0.x * a[j][0] + k0.y * a[j][1];
-                ka1 += k1.x * a[j][2] + k1.y * a[j][3];
-                dk[j][0] += a[j][0]; dk[j][1] += a[j][1]; dk[j][2] += a[j][2]; dk[j][3] += a[j][3];
-            }
-            ka0 = quad_sum(ka0); ka1 = quad_sum(ka1);
-            if (t == 0) {
-                S.row[2][part][i0] = ka0; S.row[2][part][i1] = ka1;
-            }
-        }
-        __syncthreads();               // dS and X have been read, all sums are there
-        if (follows) fetch_second(then, then_h);
-        // dQ += dP K, dK += dP^T Q + dB K + dB^T K
-#pragma unroll
-        for (int ks = 0; ks < 4; ++ks) {
-            uint32_t fpn[4], fbn[4], fpt[4], fbt[4];
-            if (ks <= rw) {            // rows reach tokens up to their own
-                ldsm(fpn, a_addr<128>(sdp, 16 * rw, 2 * ks, lane));
-                ldsm(fbn, a_addr<128>(sdb, 16 * rw, 2 * ks, lane));
-            }
-            if (ks >= rw) {            // transposed: from their own on
-                ldsm_t(fpt, b_addr<128>(sdp, 16 * ks, 2 * rw, lane));
-                ldsm_t(fbt, b_addr<128>(sdb, 16 * ks, 2 * rw, lane));
-            }
-#pragma unroll
-            for (int np = 0; np < 2; ++np) {
-                uint32_t b[4];
-                ldsm_t(b, a_addr<256>(sk, 16 * ks, 4 * part + 2 * np, lane));
-                if (ks <= rw) {
-                    mma_f16(dq[2 * np], fpn, b[0], b[1]);
-                    mma_f16(dq[2 * np + 1], fpn, b[2], b[3]);
-                    mma_f16(dk[2 * np], fbn, b[0], b[1]);
-                    mma_f16(dk[2 * np + 1], fbn, b[2], b[3]);
+                if (i0 < rows) {
+                    const size_t o = ((size_t)(tok + i0) * I.Hk + hk) * kDim + ch;
+                    *reinterpret_cast<uint32_t*>(B.dq + o) = pack_bf16(back * dq[j][0], back * dq[j][1]);
+                    *reinterpret_cast<uint32_t*>(B.dk + o) = pack_bf16(back * dk[j][0], back * dk[j][1]);
                 }
-                if (ks >= rw) {
-                    mma_f16(dk[2 * np], fbt, b[0], b[1]);
-                    mma_f16(dk[2 * np + 1], fbt, b[2], b[3]);
-                    ldsm_t(b, a_addr<256>(sq, 16 * ks, 4 * part + 2 * np, lane));
-                    mma_f16(dk[2 * np], fpt, b[0], b[1]);
-                    mma_f16(dk[2 * np + 1], fpt, b[2], b[3]);
+                if (i1 < rows) {
+                    const size_t o = ((size_t)(tok + i1) * I.Hk + hk) * kDim + ch;
+                    *reinterpret_cast<uint32_t*>(B.dq + o) = pack_bf16(back * dq[j][2], back * dq[j][3]);
+                    *reinterpret_cast<uint32_t*>(B.dk + o) = pack_bf16(back * dk[j][2], back * dk[j][3]);
                 }
             }
         }
-        // gates: two tokens per lane of one warp
-        if (w == 0) {
-            float dgv[2], ka[2];
-#pragma unroll
-            for (int m = 0; m < 2; ++m) {
-                const int j = 2 * lane + m;
-                const auto parts = [&](const float (&x)[kParts][kC]) { return (x[0][j] + x[1][j]) + (x[2][j] + x[3][j]); };
-                const float qa = parts(S.row[0]), kz = parts(S.row[1]), rs = parts(S.row[3]), bs = parts(S.row[4]), yv = parts(S.yv);
-                ka[m] = parts(S.row[2]);
-                const float cs = S.col[0][j] + S.col[1][j] + S.col[2][j] + S.col[3][j];
-                dgv[m] = qa - ka[m] - gate[kGateBe + j] * kz + rs - cs;
-                if (j < rows)
-                    store_gate(B.dbeta, I.gate_dtype, (size_t)(tok + j) * I.Hv + h,
-                               back * (yv - gate[kGateE + j] * kz + bs));
-            }
-            float all = ka[0] + ka[1];
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xFFFFFFFFu, all, o);
-            float dot = 0.0f;
-#pragma unroll
-            for (int i = 0; i < kChunkThreads / 32; ++i) dot += S.dot[i];
-            if (lane == 31) dgv[1] += all + gate[kGateAll] * dot;
-            float x = dgv[0] + dgv[1];         // sums from a token to the chunk's last
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const float y = __shfl_down_sync(0xFFFFFFFFu, x, o);
-                if (lane + o < 32) x += y;
-            }
-            if (2 * lane < rows) store_gate(B.dg, I.gate_dtype, (size_t)(tok + 2 * lane) * I.Hv + h, back * x);
-            if (2 * lane + 1 < rows)
-                store_gate(B.dg, I.gate_dtype, (size_t)(tok + 2 * lane + 1) * I.Hv + h, back * (x - dgv[0]));
-        }
-    }
-    // dQ and dK as bf16 rows
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const int ch = 32 * part + 8 * j + 2 * t;
-        if (i0 < rows) {
-            const size_t o = ((size_t)(tok + i0) * I.Hk + hk) * kDim + ch;
-            *reinterpret_cast<uint32_t*>(B.dq + o) = pack_bf16(back * dq[j][0], back * dq[j][1]);
-            *reinterpret_cast<uint32_t*>(B.dk + o) = pack_bf16(back * dk[j][0], back * dk[j][1]);
-        }
-        if (i1 < rows) {
-            const size_t o = ((size_t)(tok + i1) * I.Hk + hk) * kDim + ch;
-            *reinterpret_cast<uint32_t*>(B.dq + o) = pack_bf16(back * dq[j][2], back * dq[j][3]);
-            *reinterpret_cast<uint32_t*>(B.dk + o) = pack_bf16(back * dk[j][2], back * dk[j][3]);
-        }
-    }
     }
 }
 
@@ -506,10 +548,19 @@ __global__ void __launch_bounds__(kChunkThreads, 1) gdr_bwd_chunk_kernel(GdrBack
 
 cudaError_t launch_gdr_bwd_chunk(const GdrBackward& B, int sms, cudaStream_t s) {
     if (B.fwd.chunks.total == 0) return cudaSuccess;
-    const cudaError_t e = allow_smem<gdr_bwd_chunk_kernel>(sizeof(ChunkSmem));
-    if (e != cudaSuccess) return e;
     const long long pairs = (long long)B.fwd.chunks.total * B.fwd.in.Hk;
-    gdr_bwd_chunk_kernel<<<(unsigned)std::min<long long>(pairs, sms), kChunkThreads, sizeof(ChunkSmem), s>>>(B);
+    const int share = B.fwd.in.Hv / B.fwd.in.Hk;
+    int split = 1;                         // at most 8 CTAs, as many as there are heads and SMs for
+    while (split < 8 && 2 * split <= share && pairs * 2 * split <= sms) split *= 2;
+    if (split > 1) {
+        const cudaError_t e = allow_smem<gdr_bwd_chunk_kernel<true>>(sizeof(ChunkSmem));
+        if (e != cudaSuccess) return e;
+        return launch_clusters(gdr_bwd_chunk_kernel<true>, (unsigned)(pairs * split), kChunkThreads, sizeof(ChunkSmem),
+                               (unsigned)split, s, B, split);
+    }
+    const cudaError_t e = allow_smem<gdr_bwd_chunk_kernel<false>>(sizeof(ChunkSmem));
+    if (e != cudaSuccess) return e;
+    gdr_bwd_chunk_kernel<false><<<(unsigned)std::min<long long>(pairs, sms), kChunkThreads, sizeof(ChunkSmem), s>>>(B, 1);
     return cudaGetLastError();
 }
 

@@ -220,8 +220,8 @@ struct GdrBackward {      // what the backward pass has besides
 cudaError_t launch_gdr_bwd_chain(const GdrBackward& P, cudaStream_t s);
 cudaError_t launch_gdr_bwd_chunk(const GdrBackward& P, int sms, cudaStream_t s);
 cudaError_t launch_gdr_map(const GdrInputs& in, int* first, int* order, int* valid, int* err, cudaStream_t s);
-cudaError_t launch_gdr_prep(const GdrChunked& P, cudaStream_t s);
-cudaError_t launch_gdr_prep(const GdrBackward& P, cudaStream_t s);   // finds the largest gradients too
+cudaError_t launch_gdr_prep(const GdrChunked& P, int sms, cudaStream_t s);
+cudaError_t launch_gdr_prep(const GdrBackward& P, int sms, cudaStream_t s);   // finds the largest gradients too
 cudaError_t launch_gdr_chain(const GdrChunked& P, cudaStream_t s);
 
 }  // namespace kda

@@ -89,7 +89,8 @@ __global__ void __launch_bounds__(kMapThreads) gdr_map_kernel(GdrInputs I, int* 
 }
 
 // ---- prep -------------------------------------------------------------------------------
-// One CTA of 4 warps per (chunk, query/key head).  Warp w forms rows 16 w .. 16 w + 15 of
+// One CTA of 4 warps per (chunk, query/key head), or `split` of them that share the value heads
+// where all are on the GPU at once.  Warp w forms rows 16 w .. 16 w + 15 of
 // K K^T and Q K^T on tensor cores (bf16 data, fp32 sums; kept in registers for all value
 // heads of the group), and per value head: the gates' running sum, A and P, and
 // T = (I + A)^-1: the four 16 x 16 diagonal blocks by forward substitution in fp32 (a lane
@@ -98,7 +99,7 @@ __global__ void __launch_bounds__(kMapThreads) gdr_map_kernel(GdrInputs I, int* 
 //
 // Bound by memory (K and Q once, 16 KB of T and P out per value head) once enough CTAs share
 // an SM to cover each other's chains of small steps: A, T and P live where K and Q were.
-constexpr int kPrepThreads = 128;
+constexpr int kPrepThreads = 128, kPrepPerSm = 5;
 constexpr int kLd = 68;               // row length of the fp32 tile: rows 4 banks apart
 
 struct PrepSmem {
@@ -180,7 +181,7 @@ __device__ __forceinline__ void put_negative(float (*M)[kLd], int row, int col, 
 // Backward: the largest magnitude of the gradients that enter a (sequence, key head), by all its
 // chunks' CTAs: scale dO of the chunk's tokens and a share of the last state's gradient.
 __device__ __forceinline__ void largest_gradient(const GdrInputs& I, const GdrGrads& B, const Span& span, int n, int c, int hk,
-                                                 unsigned* shared_top, int tid) {
+                                                 int part, int split, unsigned* shared_top, int tid) {
     const int share = I.Hv / I.Hk, rows = min(kC, span.len - c * kC), units = share * 16;   // 16-byte units of a token
     const __nv_bfloat16* src = B.dout + ((span.start + (long long)c * kC) * I.Hv + hk * share) * kDim;
     const auto bits = [](unsigned u) {         // two bf16 values; NaN compares above infinity
@@ -188,7 +189,7 @@ __device__ __forceinline__ void largest_gradient(const GdrInputs& I, const GdrGr
     };
     const auto four = [&](uint4 u) { return max(max(bits(u.x), bits(u.y)), max(bits(u.z), bits(u.w))); };
     unsigned top = 0;
-    for (int at = tid & 31; at < units; at += 32) {
+    for (int at = 32 * part + (tid & 31); at < units; at += 32 * split) {
 #pragma unroll
         for (int i = 0; i < kC; i += 8 * (kPrepThreads / 32)) {
             uint4 u[8];
@@ -206,9 +207,9 @@ __device__ __forceinline__ void largest_gradient(const GdrInputs& I, const GdrGr
         const bool f32 = B.dfinal_dtype == KDA_F32;
         const size_t base = ((size_t)n * I.Hv + hk * share) * kDim * kDim, count = (size_t)share * kDim * kDim;
         const size_t per = f32 ? 4 : 8;        // values of 16 bytes
-        const size_t step = (size_t)((span.len + kC - 1) / kC) * kPrepThreads;
+        const size_t step = (size_t)((span.len + kC - 1) / kC) * split * kPrepThreads;
         const uint4* src = reinterpret_cast<const uint4*>(static_cast<const unsigned char*>(B.dfinal) + base * (16 / per));
-        for (size_t i = (size_t)c * kPrepThreads + tid; i < count / per; i += 8 * step) {
+        for (size_t i = ((size_t)c * split + part) * kPrepThreads + tid; i < count / per; i += 8 * step) {
             uint4 u[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) u[j] = i + j * step < count / per ? __ldg(src + i + j * step) : make_uint4(0u, 0u, 0u, 0u);
@@ -225,13 +226,14 @@ __device__ __forceinline__ void largest_gradient(const GdrInputs& I, const GdrGr
     if (tid == 0) atomicMax(&B.amax[(size_t)n * I.Hk + hk], max(max(shared_top[0], shared_top[1]), max(shared_top[2], shared_top[3])));
 }
 
-template <bool kGrads>
-__global__ void __launch_bounds__(kPrepThreads, 5) gdr_prep_kernel(GdrChunked P, GdrGrads B) {
+template <bool kGrads, bool kSplit>
+__global__ void __launch_bounds__(kPrepThreads, kPrepPerSm) gdr_prep_kernel(GdrChunked P, GdrGrads B, int ways) {
+    const int split = kSplit ? ways : 1;
     extern __shared__ __align__(128) unsigned char raw[];
     PrepSmem& S = *reinterpret_cast<PrepSmem*>(raw);
     const GdrInputs& I = P.in;
     const int tid = threadIdx.x, lane = tid & 31, g = lane >> 2, t = lane & 3;
-    const int chunk = blockIdx.x, hk = blockIdx.y;
+    const int chunk = blockIdx.x, hk = blockIdx.y / split, part = blockIdx.y % split;
     // rows of this warp; the last ones have four times the work of the first, so the warps of
     // one scheduler take different ones in different CTAs
     const int w = ((tid >> 5) + chunk) & 3;
@@ -260,8 +262,8 @@ __global__ void __launch_bounds__(kPrepThreads, 5) gdr_prep_kernel(GdrChunked P,
             b1 = load_gate(I.beta, I.gate_dtype, at + I.Hv);
         }
     };
-    fetch_gates(hk * share);
-    if (kGrads) largest_gradient(I, B, span, n, c, hk, S.top, tid);
+    fetch_gates(hk * share + part);
+    if (kGrads) largest_gradient(I, B, span, n, c, hk, part, split, S.top, tid);
     cp_async_wait<0>();
     __syncthreads();
     // rows 16 w ..  of K K^T and Q K^T, columns 0 .. 16 w + 15
@@ -286,7 +288,7 @@ __global__ void __launch_bounds__(kPrepThreads, 5) gdr_prep_kernel(GdrChunked P,
             mma_bf16(qk[2 * np + 1], aq, b[2], b[3]);
         }
     }
-    for (int h = hk * share; h < (hk + 1) * share; ++h) {
+    for (int h = hk * share + part; h < (hk + 1) * share; h += split) {
         __syncthreads();               // K and Q, or the last head's tiles, have been read
         unsigned char* block = P.blocks + ((size_t)chunk * I.Hv + h) * kBlockBytes;
         if (w == 0) {
@@ -315,7 +317,7 @@ __global__ void __launch_bounds__(kPrepThreads, 5) gdr_prep_kernel(GdrChunked P,
             reinterpret_cast<float2*>(gates + kGateEnd)[lane] = make_float2(ex2_approx(last - x0), ex2_approx(last - x));
             reinterpret_cast<float2*>(gates + kGateG)[lane] = make_float2(x0, x);
             if (lane == 0) gates[kGateAll] = ex2_approx(last);
-            if (h + 1 < (hk + 1) * share) fetch_gates(h + 1);
+            if (h + split < (hk + 1) * share) fetch_gates(h + split);
         }
         __syncthreads();
         // A in fp32 and P in fp16
@@ -430,16 +432,25 @@ cudaError_t launch_gdr_map(const GdrInputs& in, int* first, int* order, int* val
     return cudaGetLastError();
 }
 
-template <bool kGrads>
-static cudaError_t launch_prep(const GdrChunked& P, const GdrGrads& B, cudaStream_t s) {
-    if (P.chunks.total == 0) return cudaSuccess;
-    const cudaError_t e = allow_smem<gdr_prep_kernel<kGrads>>(sizeof(PrepSmem));
+template <bool kGrads, bool kSplit>
+static cudaError_t launch_prep(const GdrChunked& P, const GdrGrads& B, int split, cudaStream_t s) {
+    const cudaError_t e = allow_smem<gdr_prep_kernel<kGrads, kSplit>>(sizeof(PrepSmem));
     if (e != cudaSuccess) return e;
-    gdr_prep_kernel<kGrads><<<dim3(P.chunks.total, P.in.Hk), kPrepThreads, sizeof(PrepSmem), s>>>(P, B);
+    gdr_prep_kernel<kGrads, kSplit><<<dim3(P.chunks.total, P.in.Hk * split), kPrepThreads, sizeof(PrepSmem), s>>>(P, B, split);
     return cudaGetLastError();
 }
+template <bool kGrads>
+static cudaError_t launch_prep(const GdrChunked& P, const GdrGrads& B, int sms, cudaStream_t s) {
+    if (P.chunks.total == 0) return cudaSuccess;
+    const int share = P.in.Hv / P.in.Hk;
+    int split = 1;
+    while (2 * split <= share && (long long)P.chunks.total * P.in.Hk * 2 * split <= (long long)kPrepPerSm * sms &&
+           P.in.Hk * 2 * split <= 65535)
+        split *= 2;
+    return split > 1 ? launch_prep<kGrads, true>(P, B, split, s) : launch_prep<kGrads, false>(P, B, 1, s);
+}
 
-cudaError_t launch_gdr_prep(const GdrChunked& P, cudaStream_t s) { return launch_prep<false>(P, {}, s); }
-cudaError_t launch_gdr_prep(const GdrBackward& B, cudaStream_t s) { return launch_prep<true>(B.fwd, B.in, s); }
+cudaError_t launch_gdr_prep(const GdrChunked& P, int sms, cudaStream_t s) { return launch_prep<false>(P, {}, sms, s); }
+cudaError_t launch_gdr_prep(const GdrBackward& B, int sms, cudaStream_t s) { return launch_prep<true>(B.fwd, B.in, sms, s); }
 
 }  // namespace kda

@@ -12,6 +12,7 @@
 // those bytes, or for few sequences by latency.  The division is IEEE's and rest is one
 // subtraction, so the scores, and the winner, do not depend on how the row is split; ties go to
 // the lowest index.
+#include "kda_cluster.cuh"
 #include "kda_host.cuh"
 
 namespace kda {
@@ -82,13 +83,6 @@ __device__ int drafts_kept(const VerifyProblem& P, int n, int lane, int& count) 
     return count < 0 || count > P.D ? -1 : count;
 }
 
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;\n" ::: "memory"); }
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;\n" ::: "memory"); }
-__device__ __forceinline__ unsigned cluster_rank() {
-    unsigned r;
-    asm("mov.u32 %0, %%cluster_ctarank;\n" : "=r"(r));
-    return r;
-}
 // writes to the same variable of another CTA of the cluster
 __device__ __forceinline__ void put(unsigned long long* p, unsigned rank, unsigned long long x) {
     const unsigned at = (unsigned)__cvta_generic_to_shared(p);
@@ -189,16 +183,7 @@ cudaError_t launch(const VerifyProblem& P, int split, cudaStream_t s) {
     static const cudaError_t allowed =         // clusters of more than 8 CTAs
         cudaFuncSetAttribute(verify_kernel<T, VEC>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (allowed != cudaSuccess) return allowed;
-    cudaLaunchConfig_t cfg{};
-    cudaLaunchAttribute at{};
-    at.id = cudaLaunchAttributeClusterDimension;
-    at.val.clusterDim = {(unsigned)split, 1, 1};
-    cfg.gridDim = dim3((unsigned)(P.N * split));
-    cfg.blockDim = dim3(kVerThreads);
-    cfg.stream = s;
-    cfg.attrs = &at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, verify_kernel<T, VEC>, P, split);
+    return launch_clusters(verify_kernel<T, VEC>, (unsigned)(P.N * split), kVerThreads, 0, (unsigned)split, s, P, split);
 }
 
 // CTAs per sequence: twice the SMs in all if the rows are long enough for that
