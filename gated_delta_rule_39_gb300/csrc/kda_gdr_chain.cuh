@@ -15,7 +15,7 @@
 // exact), so that between two products the state warps only round an accumulator.
 //
 // Warps: 8 state warps (lane quarter w % 4, half of the columns each) do that rounding; one
-// warp issues the MMAs, those that the chain does not need where it waits for something else;
+// warp issues the MMAs, those that the chain does not need behind the state's update;
 // 4 warps bring in keys, values, T and P of the next chunks, 4 the queries, and 4 write the
 // outputs.  Every role's loop is kept small: with the MMAs issued from a state warp, the
 // others' jumps over that code cost 200 cycles each (instruction cache misses).
@@ -37,8 +37,8 @@ constexpr int kFirstKeys = kStateWarps + kOutWarps, kFirstQueries = kFirstKeys +
 constexpr int kChainThreads = 32 * (kMmaWarp + 4);   // whole warpgroups: three warps of the last are idle
 // registers of a thread: 80 at launch, then by role (2 x 112 + 64 + 72 + 80 + 40 = 6 x 80)
 constexpr int kStateRegs = 112, kOutRegs = 64, kKeyRegs = 72, kMmaRegs = 40;
-// tensor memory columns; O alternates between two buffers
-constexpr uint32_t kTmS = 0, kTmS16 = 128, kTmAcc = 192, kTmR16 = 256, kTmX16 = 288, kTmO = 320, kTmCols = 512;
+// tensor memory columns; S16 and O alternate between two buffers
+constexpr uint32_t kTmS = 0, kTmS16 = 128, kTmAcc = 256, kTmR16 = 320, kTmX16 = 352, kTmO = 384, kTmCols = 512;
 
 struct ChainSmem {
     struct Stage {
@@ -136,8 +136,7 @@ __device__ inline void queries(const GdrChunked& P, ChainSmem& S, const Span& sp
     prefetch_rows(I.q, I.q_stride, span, hk * kDim, 1, p);
     prefetch_rows(I.q, I.q_stride, span, hk * kDim, 2, p);
     for (int c = 0; c < nch; ++c) {
-        // the update of chunk c - 1 is over, and so is the product with its queries before it
-        if (c > 0 && !bar_wait(&S.s_done, (unsigned)((c - 1) & 1), P.err)) return;
+        if (c > 0 && !bar_wait(&S.o_done[(c - 1) & 1], (unsigned)(((c - 1) >> 1) & 1), P.err)) return;   // the last ones have been used
 #pragma unroll
         for (int i = 0; i < kTokenRows; ++i)
             *reinterpret_cast<uint4*>(S.q + dst + 1024 * i) = scaled_half8(q.x[i], __shfl_sync(0xFFFFFFFFu, ga, (lane & 16) + i));
@@ -173,38 +172,31 @@ __device__ void issue(const GdrChunked& P, ChainSmem& S, int nch, uint32_t tmem)
         for (int k = 0; k < 4; ++k)
             tc::mma_ss_on(tmem + kTmAcc, dv + kstep_mn(k), de + kstep_k(k, 0), kId64 | tc::kIdBf16 | tc::kIdMnA, k > 0, on);
     };
-    // the outputs' second product, X16 P^T, after which the chunk's stage is free
-    const auto finish = [&](int c) {
-        const uint32_t on = tc::elect();
-        product_k<4>(tmem + kTmO + 64 * uniform(c & 1), tmem + kTmX16, stage_of(c) + offsetof(ChainSmem::Stage, tp) + kTileBytes, kId64, true, on);
-        tc::commit_on(smem_u32(&S.o_done[c & 1]), on);
-        tc::commit_on(smem_u32(&S.empty[c % kStages]), on);
-    };
     if (!there(0)) return;
     begin(0);
     for (int c = 0; c < nch; ++c) {
-        const unsigned turn = (unsigned)(c & 1);
-        const uint32_t stage = stage_of(c), on = tc::elect();
+        const unsigned turn = (unsigned)(c & 1), phase = (unsigned)((c >> 1) & 1);
+        const uint32_t stage = stage_of(c), s16 = tmem + kTmS16 + 64 * uniform(turn), on = tc::elect();
         if (!wait(S.s16, turn)) return;
-        product_k<8>(tmem + kTmAcc, tmem + kTmS16, stage + offsetof(ChainSmem::Stage, kn), kId64, true, on);
+        product_k<8>(tmem + kTmAcc, s16, stage + offsetof(ChainSmem::Stage, kn), kId64, true, on);
         tc::commit_on(smem_u32(&S.acc), on);
-        if (!kSave) {
-            if (c > 0) finish(c - 1);
-            // the queries are there, the outputs of chunk c - 2 have been read
-            if (!wait(S.q_full, turn) || (c >= 2 && !wait(S.o_free[turn], (unsigned)(((c >> 1) - 1) & 1)))) return;
-        }
         if (!wait(S.r16, turn)) return;
         product_k<4>(tmem + kTmAcc, tmem + kTmR16, stage + offsetof(ChainSmem::Stage, tp), kId64, false, on);
         tc::commit_on(smem_u32(&S.x), on);
-        if (!kSave) product_k<8>(tmem + kTmO + 64 * uniform(turn), tmem + kTmS16, smem_u32(S.q), kId64, false, on);
         if (c + 1 < nch && !there(c + 1)) return;
         if (!wait(S.x16, turn)) return;
         product_mn(tmem + kTmS, tmem + kTmX16, stage + offsetof(ChainSmem::Stage, kd), kId128, true, on);
         tc::commit_on(smem_u32(&S.s_done), on);
-        if (kSave) tc::commit_on(smem_u32(&S.empty[c % kStages]), on);
         if (c + 1 < nch) begin(c + 1);
+        if (!kSave) {                         // outputs, once the queries are there and those of chunk c - 2 read
+            if (!wait(S.q_full, turn) || (c >= 2 && !wait(S.o_free[turn], phase ^ 1u))) return;
+            const uint32_t o = tmem + kTmO + 64 * uniform(turn);
+            product_k<8>(o, s16, smem_u32(S.q), kId64, false, on);
+            product_k<4>(o, tmem + kTmX16, stage + offsetof(ChainSmem::Stage, tp) + kTileBytes, kId64, true, on);
+            tc::commit_on(smem_u32(&S.o_done[turn]), on);
+        }
+        tc::commit_on(smem_u32(&S.empty[c % kStages]), on);
     }
-    if (!kSave) finish(nch - 1);
 }
 
 // ---- state warps ----------------------------------------------------------------------------
@@ -231,7 +223,7 @@ __device__ void states(const GdrChunked& P, ChainSmem& S, const Span& span, int 
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             to_half<16>(x[i], f[i]);
-            tc::st16(tl + kTmS16 + 32 * half + 16 * i, f[i]);
+            tc::st16(tl + kTmS16 + 64 * turn + 32 * half + 16 * i, f[i]);
             scale32(x[i], d);
             tc::st32(tl + kTmS + 64 * half + 32 * i, x[i]);
         }
