@@ -172,8 +172,7 @@ def kda_qk_norm_bwd(q, k, dq_out, dk_out, norm: str = "l2", eps: float = 1e-6, q
                                           positions)
     _dense(dq_out, "dq_out", (q.dtype,), q.shape, dev)
     _dense(dk_out, "dk_out", (q.dtype,), k.shape, dev)
-    r = {"dq": torch.empty(q.shape, dtype=q.dtype, device=dev),
-         "dk": torch.empty(k.shape, dtype=q.dtype, device=dev)}
+    r = {"dq": torch.empty_like(dq_out), "dk": torch.empty_like(dk_out)}
     if q_weight is not None:
         r["dq_weight"] = torch.empty_like(q_weight)
     if k_weight is not None:
@@ -260,10 +259,9 @@ def kda_gdr_bwd(q, k, v, g, beta, scale: float, d_out, initial_state=None, d_fin
     _dense(d_out, "d_out", (torch.bfloat16,), (B, T, Hv, V), dev)
     N, num = _sequences(cu_seqlens, B, dev)
     states = _states(dev, (N, Hv, K, V), initial_state=initial_state, d_final_state=d_final_state)
-    r = {"dq": torch.empty((B, T, Hk, K), dtype=q.dtype, device=dev),
-         "dk": torch.empty((B, T, Hk, K), dtype=q.dtype, device=dev),
-         "dv": torch.empty((B, T, Hv, V), dtype=q.dtype, device=dev),
-         "dg": torch.empty_like(g), "dbeta": torch.empty_like(beta)}
+    dense = torch.contiguous_format
+    r = {"dq": torch.empty_like(q, memory_format=dense), "dk": torch.empty_like(k, memory_format=dense),
+         "dv": torch.empty_like(d_out), "dg": torch.empty_like(g), "dbeta": torch.empty_like(beta)}
     ds = None
     if d_initial_state and initial_state is not None:
         ds = r["d_initial_state"] = torch.empty_like(initial_state)
