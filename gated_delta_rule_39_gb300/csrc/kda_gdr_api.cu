@@ -1,6 +1,7 @@
 // The C entry points of the gated delta rule with one decay per value head: checks,
 // scratch and launches (the operation and its kernels: kda_gdr.cuh).
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 
 #include "kda_gdr_chunk.cuh"
@@ -63,17 +64,20 @@ size_t plan_chunks(bool varlen, int B, int T, int N, gdr::Chunks* c) {
     return varlen ? align_up((2 * (size_t)N + 2) * sizeof(int)) : 0;
 }
 
+constexpr int kPartUnits = 1000;          // chunks x heads from which a backward pass is done in two parts
+
 // Scratch of a backward pass (bytes from its start): the map of packed sequences, the
-// largest gradients, and per (chunk, value head) a block, T, S^T, X^T, dS^T and Y^T.
+// largest gradients, states between two parts, and per (chunk, value head) a block, T, S^T, X^T, dS^T and Y^T.
 struct BwdLayout {
     gdr::Chunks chunks{};
-    size_t amax, blocks, ts, states, xs, dstates, ys, total;
+    size_t amax, carry, blocks, ts, states, xs, dstates, ys, total;
 };
 BwdLayout bwd_layout(bool varlen, int B, int T, int Hk, int Hv, int N) {
     BwdLayout L{};
     L.amax = plan_chunks(varlen, B, T, N, &L.chunks);
     const size_t units = (size_t)L.chunks.total * Hv;
-    L.blocks = L.amax + align_up((size_t)N * Hk * 4);
+    L.carry = L.amax + align_up((size_t)N * Hk * 4);
+    L.blocks = L.carry + (N == 1 && (long long)L.chunks.total * Hv >= kPartUnits ? align_up(state_bytes(1, Hv, KDA_F32)) : 0);
     L.ts = L.blocks + units * gdr::kBlockBytes;
     L.states = L.ts + units * gdr::kTileBytes;
     L.xs = align_up(L.states + units * gdr::kStateTile);
@@ -81,6 +85,183 @@ BwdLayout bwd_layout(bool varlen, int B, int T, int Hk, int Hv, int N) {
     L.ys = L.dstates + units * gdr::kStateTile;
     L.total = L.ys + units * gdr::kTokenTile + kAlign;
     return L;
+}
+
+// A second stream of this device, made once.
+cudaError_t side_stream(cudaStream_t* out) {
+    static std::atomic<cudaStream_t> made[64];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    cudaStream_t s = made[dev].load(std::memory_order_acquire);
+    if (!s) {
+        e = cudaStreamCreateWithFlags(&s, cudaStreamNonBlocking);
+        if (e != cudaSuccess) return e;
+        cudaStream_t none = nullptr;
+        if (!made[dev].compare_exchange_strong(none, s)) {     // another thread was first
+            cudaStreamDestroy(s);
+            s = none;
+        }
+    }
+    *out = s;
+    return cudaSuccess;
+}
+
+// How many chunks of one long sequence to prepare before its chains begin; the rest are prepared
+// beside them, on the SMs that the chains (one per value head) leave.  0: not worth it, or the stream is
+// being captured.  A chain takes 1.6 us per chunk and the whole GPU 0.0122 us to prepare a chunk of a
+// head, so while a chain walks a chunk the idle SMs prepare `rate` of them; of two parts the first is 1
+// in 1 + rate.  (8,192 tokens: 96 heads 359 -> 337 us, 64 heads 303 -> 273, 32
+// heads 240 -> 225.)
+int chunks_before(const GdrChunked& P, int sms, cudaStream_t s) {
+    const int units = P.in.Hv, chunks = P.chunks.total;
+    if (P.in.cu || P.in.N != 1 || chunks < 64 || (long long)chunks * units < 2500 || units >= sms - sms / 8) return 0;
+    cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+    if (cudaStreamIsCapturing(s, &capture) != cudaSuccess || capture != cudaStreamCaptureStatusNone) return 0;
+    const float rate = 1.6f / 0.0122f * (float)(sms - units) / ((float)units * (float)sms);
+    return std::max(8, (int)std::ceil((float)chunks / (1.0f + rate)));
+}
+
+// The chunks [first, first + count) of a sequence as a problem of its own.
+GdrChunked part_of(const GdrChunked& P, int first, int count) {
+    GdrChunked Q = P;
+    const long long t = (long long)first * gdr::kC;
+    const size_t gate = P.in.gate_dtype == KDA_F32 ? 4 : 2;
+    Q.in.q += t * P.in.q_stride;
+    Q.in.k += t * P.in.k_stride;
+    Q.in.v += t * P.in.v_stride;
+    Q.in.g = static_cast<const char*>(P.in.g) + (size_t)t * P.in.Hv * gate;
+    Q.in.beta = static_cast<const char*>(P.in.beta) + (size_t)t * P.in.Hv * gate;
+    Q.in.T = (int)std::min<long long>(P.in.T - t, (long long)count * gdr::kC);
+    Q.chunks.per_seq = Q.chunks.total = count;
+    Q.blocks += (size_t)first * P.in.Hv * gdr::kBlockBytes;
+    if (Q.out) Q.out += t * P.in.Hv * kDim;
+    const size_t at = (size_t)first * P.in.Hv;
+    if (Q.states) {                        // a backward pass
+        Q.states += at * gdr::kStateTile;
+        Q.xs += at * gdr::kTokenTile;
+        Q.ts += at * gdr::kTileBytes;
+    }
+    return Q;
+}
+
+// Two streams' work between two events: the second one joins the caller's again whatever happens.
+struct Fork {
+    cudaStream_t s, side = nullptr;
+    cudaEvent_t begun = nullptr, over = nullptr;
+    explicit Fork(cudaStream_t s_) : s(s_) {}
+    cudaError_t make() {
+        cudaError_t e = side_stream(&side);
+        if (e == cudaSuccess) e = cudaEventCreateWithFlags(&begun, cudaEventDisableTiming);
+        if (e == cudaSuccess) e = cudaEventCreateWithFlags(&over, cudaEventDisableTiming);
+        return e;
+    }
+    // what comes on `side` from here on follows what is on s up to now
+    cudaError_t mark() { return cudaEventRecord(begun, s); }
+    cudaError_t begin() { return cudaStreamWaitEvent(side, begun, 0); }
+    cudaError_t join() {
+        return cudaEventRecord(over, side) == cudaSuccess ? cudaStreamWaitEvent(s, over, 0) : cudaStreamSynchronize(side);
+    }
+    ~Fork() {
+        if (begun) cudaEventDestroy(begun);
+        if (over) cudaEventDestroy(over);
+    }
+};
+
+// Prep and chain in two parts, the second's prep on a stream of its own beside the first's
+// chain; `carry` holds the fp32 states between the parts.
+cudaError_t run_in_parts(const GdrChunked& P, int first, float* carry, int sms, cudaStream_t s) {
+    GdrChunked a = part_of(P, 0, first), b = part_of(P, first, P.chunks.total - first);
+    a.final_state = carry;
+    a.final_dtype = KDA_F32;
+    b.init_state = carry;
+    b.init_dtype = KDA_F32;
+    const auto prep = [&](const GdrChunked& part, cudaStream_t on) {
+        return timed_launch(KDA_KERNEL_GDR_PREP, on, [&] { return launch_gdr_prep(part, sms, on); });
+    };
+    const auto chain = [&](const GdrChunked& part) {
+        return timed_launch(KDA_KERNEL_GDR_CHAIN, s, [&] { return launch_gdr_chain(part, s); });
+    };
+    Fork fork(s);
+    cudaError_t e = fork.make();
+    if (e == cudaSuccess) e = prep(a, s);
+    if (e == cudaSuccess) e = fork.mark();
+    if (e == cudaSuccess) e = chain(a);
+    if (e == cudaSuccess) e = fork.begin();
+    if (e == cudaSuccess) {
+        e = prep(b, fork.side);
+        const cudaError_t joined = fork.join();
+        if (e == cudaSuccess) e = joined;
+    }
+    if (e == cudaSuccess) e = chain(b);
+    return e;
+}
+
+// The same for a backward pass, after prep: whether one long sequence of few heads is worth two parts,
+bool in_two_parts(const GdrInputs& in, int chunks, int sms) {
+    return !in.cu && in.N == 1 && (long long)chunks * in.Hv >= kPartUnits && 4 * in.Hv <= sms;
+}
+// and how many chunks at its end to have the gradient's chain walk first, so that the chunk kernel
+// can take them beside the rest of the chain, on the SMs that it leaves.  The gradient's chain takes 2.4
+// us per chunk, the one for the states, which has to be over by then, 1.6, and the chunk kernel on the
+// whole GPU 0.073 us per chunk and head.  (4,096 tokens: 32 heads 343 -> 329 us, 16 heads 267 -> 240; 8,192
+// tokens, 8 heads: 406 -> 355.)
+int chunks_first(const GdrBackward& B, int sms, cudaStream_t s) {
+    const int units = B.fwd.in.Hv, chunks = B.fwd.chunks.total;
+    if (!in_two_parts(B.fwd.in, chunks, sms)) return 0;
+    cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+    if (cudaStreamIsCapturing(s, &capture) != cudaSuccess || capture != cudaStreamCaptureStatusNone) return 0;
+    const float rate = 0.073f / 2.4f * (float)units * (float)sms / (float)(sms - units);
+    return std::min(chunks - 1, (int)((float)chunks * std::max(1.6f / 2.4f, 1.0f / (1.0f + rate))));
+}
+
+GdrBackward part_of(const GdrBackward& B, int first, int count) {
+    GdrBackward C = B;
+    const GdrInputs& in = B.fwd.in;
+    const size_t t = (size_t)first * gdr::kC, at = (size_t)first * in.Hv, gate = in.gate_dtype == KDA_F32 ? 4 : 2;
+    C.fwd = part_of(B.fwd, first, count);
+    C.in.dout += t * in.Hv * kDim;
+    C.dstates += at * gdr::kStateTile;
+    C.ys += at * gdr::kTokenTile;
+    C.dq += t * in.Hk * kDim;
+    C.dk += t * in.Hk * kDim;
+    C.dv += t * in.Hv * kDim;
+    C.dg = static_cast<char*>(B.dg) + t * in.Hv * gate;
+    C.dbeta = static_cast<char*>(B.dbeta) + t * in.Hv * gate;
+    return C;
+}
+
+// Chains and chunk kernel, in two parts if `last` (chunks at the end) is not 0; `carry` holds the fp32
+// gradient of the states between them.
+cudaError_t run_backward(const GdrBackward& B, int last, float* carry, int sms, cudaStream_t s) {
+    const auto chain = [&](const GdrBackward& part, const GdrChunked* states_too) {
+        return timed_launch(KDA_KERNEL_GDR_BWD_CHAIN, s, [&] { return launch_gdr_bwd_chain(part, states_too, s); });
+    };
+    const auto chunk = [&](const GdrBackward& part, int on_sms, cudaStream_t on) {
+        return timed_launch(KDA_KERNEL_GDR_BWD_CHUNK, on, [&] { return launch_gdr_bwd_chunk(part, on_sms, on); });
+    };
+    if (!last) {
+        const cudaError_t e = chain(B, &B.fwd);
+        return e == cudaSuccess ? chunk(B, sms, s) : e;
+    }
+    const int first = B.fwd.chunks.total - last;
+    GdrBackward a = part_of(B, 0, first), b = part_of(B, first, last);
+    a.in.dfinal = b.dinit = carry;
+    a.in.dfinal_dtype = b.dinit_dtype = KDA_F32;
+    Fork fork(s);
+    cudaError_t e = fork.make();
+    if (e == cudaSuccess) e = chain(b, &B.fwd);
+    if (e == cudaSuccess) e = fork.mark();
+    if (e == cudaSuccess) e = chain(a, nullptr);
+    if (e == cudaSuccess) e = fork.begin();
+    if (e == cudaSuccess) {
+        e = chunk(b, sms - B.fwd.in.Hv, fork.side);
+        if (e == cudaSuccess) e = chunk(a, sms, s);
+        const cudaError_t joined = fork.join();
+        if (e == cudaSuccess) e = joined;
+    }
+    return e;
 }
 
 }  // namespace
@@ -172,8 +353,10 @@ int kda_gdr_fwd(const void* q, const void* k, const void* v, const void* g, cons
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const size_t map_bytes = plan_chunks(varlen, B, T, N, &P.chunks);
     unsigned char* scratch = nullptr;
+    const size_t block_bytes = align_up(map_bytes + (size_t)P.chunks.total * Hv * gdr::kBlockBytes);
+    const int first_part = chunks_before(P, sms, s);
     cudaError_t e = cudaMallocAsync(reinterpret_cast<void**>(&scratch),
-                                    map_bytes + (size_t)P.chunks.total * Hv * gdr::kBlockBytes + kAlign, s);
+                                    block_bytes + (first_part ? state_bytes(1, Hv, KDA_F32) : 0) + kAlign, s);
     if (e != cudaSuccess) return cuda_fail(KDA_ERR_ALLOC, e);
     P.blocks = scratch + map_bytes;
     if (varlen) {
@@ -184,9 +367,13 @@ int kda_gdr_fwd(const void* q, const void* k, const void* v, const void* g, cons
         e = timed_launch(KDA_KERNEL_GDR_MAP, s,
                          [&] { return launch_gdr_map(P.in, first, first + N + 2, first + N + 1, P.err, s); });
     }
-    if (e == cudaSuccess) e = timed_launch(KDA_KERNEL_GDR_PREP, s, [&] { return launch_gdr_prep(P, sms, s); });
-    if (e == cudaSuccess)
-        e = timed_launch(KDA_KERNEL_GDR_CHAIN, s, [&] { return launch_gdr_chain(P, s); });
+    if (first_part) {
+        e = run_in_parts(P, first_part, reinterpret_cast<float*>(scratch + block_bytes), sms, s);
+    } else {
+        if (e == cudaSuccess) e = timed_launch(KDA_KERNEL_GDR_PREP, s, [&] { return launch_gdr_prep(P, sms, s); });
+        if (e == cudaSuccess)
+            e = timed_launch(KDA_KERNEL_GDR_CHAIN, s, [&] { return launch_gdr_chain(P, s); });
+    }
     cudaFreeAsync(scratch, s);
     if (e != cudaSuccess) return cuda_fail(KDA_ERR_LAUNCH, e);
     return KDA_OK;
@@ -277,9 +464,7 @@ int kda_gdr_bwd(const void* q, const void* k, const void* v, const void* g, cons
     if (e == cudaSuccess) e = cudaMemsetAsync(P.in.amax, 0, (size_t)N * Hk * 4, s);
     if (e == cudaSuccess) e = timed_launch(KDA_KERNEL_GDR_PREP, s, [&] { return launch_gdr_prep(P, sms, s); });
     if (e == cudaSuccess)
-        e = timed_launch(KDA_KERNEL_GDR_BWD_CHAIN, s, [&] { return launch_gdr_bwd_chain(P, s); });
-    if (e == cudaSuccess)
-        e = timed_launch(KDA_KERNEL_GDR_BWD_CHUNK, s, [&] { return launch_gdr_bwd_chunk(P, sms, s); });
+        e = run_backward(P, chunks_first(P, sms, s), reinterpret_cast<float*>(scratch + L.carry), sms, s);
     cudaFreeAsync(scratch, s);
     if (e != cudaSuccess) return cuda_fail(KDA_ERR_LAUNCH, e);
     return KDA_OK;

@@ -338,28 +338,28 @@ __device__ __forceinline__ void back_run(const GdrBackward& B, BackSmem& S, int 
 static_assert(kBackThreads == chain::kChainThreads, "one launch for both chains");
 
 // Both chains of a (sequence, value head), a CTA each: the gradient's and the one that computes the
-// states again do not need each other, and with both in one launch a sequence's time is the
-// longer one's, not the sum.  The longer ones, the gradient's, come first.
-__global__ void __launch_bounds__(kBackThreads, 1) gdr_bwd_chain_kernel(GdrBackward B, const __grid_constant__ CUtensorMap vmap) {
+// states again (where `states_too`) do not need each other, and with both in one launch a
+// sequence's time is the longer one's, not the sum.  The longer ones, the gradient's, come first.
+__global__ void __launch_bounds__(kBackThreads, 1) gdr_bwd_chain_kernel(GdrBackward B, GdrChunked F, const __grid_constant__ CUtensorMap vmap) {
     extern __shared__ __align__(1024) unsigned char raw[];
     const GdrInputs& I = B.fwd.in;
     if (I.cu && !*I.valid) return;
-    const int units = gridDim.x / 2, unit = blockIdx.x % units, n = sequence_of(B.fwd.chunks, unit / I.Hv), h = unit % I.Hv;
+    const int units = I.N * I.Hv, unit = blockIdx.x % units, n = sequence_of(B.fwd.chunks, unit / I.Hv), h = unit % I.Hv;
     if (blockIdx.x < units) back_run(B, aligned_smem<BackSmem>(raw), n, h);
-    else chain::run<true>(B.fwd, vmap, aligned_smem<chain::ChainSmem>(raw), n, h);
+    else chain::run<true>(F, vmap, aligned_smem<chain::ChainSmem>(raw), n, h);
 }
 
 }  // namespace
 
-cudaError_t launch_gdr_bwd_chain(const GdrBackward& B, cudaStream_t s) {
+cudaError_t launch_gdr_bwd_chain(const GdrBackward& B, const GdrChunked* states_too, cudaStream_t s) {
     const long long units = (long long)B.fwd.in.N * B.fwd.in.Hv;
     if (units == 0) return cudaSuccess;
     constexpr size_t smem = (sizeof(BackSmem) > sizeof(chain::ChainSmem) ? sizeof(BackSmem) : sizeof(chain::ChainSmem)) + 1024;
     CUtensorMap vmap{};
     cudaError_t e = allow_smem<gdr_bwd_chain_kernel>(smem);
-    if (e == cudaSuccess) e = chain::values_map(B.fwd, &vmap);
+    if (e == cudaSuccess && states_too) e = chain::values_map(*states_too, &vmap);
     if (e != cudaSuccess) return e;
-    gdr_bwd_chain_kernel<<<(unsigned)(2 * units), kBackThreads, smem, s>>>(B, vmap);
+    gdr_bwd_chain_kernel<<<(unsigned)(states_too ? 2 * units : units), kBackThreads, smem, s>>>(B, states_too ? *states_too : B.fwd, vmap);
     return cudaGetLastError();
 }
 

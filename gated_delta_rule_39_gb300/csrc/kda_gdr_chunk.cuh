@@ -217,7 +217,9 @@ struct GdrBackward {      // what the backward pass has besides
     int dinit_dtype;
 };
 
-cudaError_t launch_gdr_bwd_chain(const GdrBackward& P, cudaStream_t s);
+// the gradient's chain, and with it the one that computes the states of `states_too` again (or nullptr)
+cudaError_t launch_gdr_bwd_chain(const GdrBackward& P, const GdrChunked* states_too, cudaStream_t s);
+// on `sms` SMs
 cudaError_t launch_gdr_bwd_chunk(const GdrBackward& P, int sms, cudaStream_t s);
 cudaError_t launch_gdr_map(const GdrInputs& in, int* first, int* order, int* valid, int* err, cudaStream_t s);
 cudaError_t launch_gdr_prep(const GdrChunked& P, int sms, cudaStream_t s);
