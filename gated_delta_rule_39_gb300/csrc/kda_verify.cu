@@ -93,7 +93,7 @@ __device__ __forceinline__ void put(unsigned long long* p, unsigned rank, unsign
 // winners.  Every warp decides for itself which drafts are kept, with the first noise on its way.
 template <typename T, int VEC>
 __global__ void __launch_bounds__(kVerThreads, 2) verify_kernel(VerifyProblem P, int split) {
-    constexpr int kUnits = 8 / VEC;            // of a thread at a time
+    constexpr int kUnits = VEC == 1 ? 8 : sizeof(T) == 2 ? 2 : 1;      // of a thread at a time
     __shared__ unsigned long long s_best[2][kVerThreads / 32], s_rank[2][kMaxSplit];
     const int n = blockIdx.x / split, tid = threadIdx.x, lane = tid & 31;
     const unsigned rank = cluster_rank();
@@ -196,10 +196,10 @@ int split_of(int N, int V, int sms) {
 template <typename T>
 cudaError_t launch(const VerifyProblem& P, int sms, cudaStream_t s) {
     const int split = split_of(P.N, P.V, sms);
-    // four elements at a time where every row begins on that boundary
-    if (P.V % 4 == 0 && aligned16(P.noise) && reinterpret_cast<uintptr_t>(P.target) % (4 * sizeof(T)) == 0 &&
-        reinterpret_cast<uintptr_t>(P.draft) % (4 * sizeof(T)) == 0)
-        return launch<T, 4>(P, split, s);
+    // eight elements at a time where every row begins on that boundary
+    const auto fits = [](const void* p, size_t bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; };
+    if (P.V % 8 == 0 && fits(P.noise, 32) && fits(P.target, 8 * sizeof(T)) && fits(P.draft, 8 * sizeof(T)))
+        return launch<T, 8>(P, split, s);
     return launch<T, 1>(P, split, s);
 }
 
