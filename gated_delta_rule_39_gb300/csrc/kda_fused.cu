@@ -35,7 +35,7 @@
 #include <cstring>
 #include <mutex>
 
-#include "kda_host.cuh"
+#include "kda_internal.cuh"
 #include "kda_tcgen05.cuh"
 
 // Every wait of the kernel is bounded.  A pipeline wait gives up after KDA_SPIN_LIMIT
@@ -1325,7 +1325,9 @@ std::atomic<int> g_sms[64];   // SM count per device, 0 until read
 PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 std::once_flag g_encode_once;
 
-bool find_encode() {
+// [rows][H][128] bf16 viewed as a 3-D tensor (channel, head, row); boxes of
+// 64 channels x 1 head x 16 rows, 128-byte swizzle (one 128-byte row per token)
+cudaError_t encode_rows(CUtensorMap* map, const void* base, int H, long long rows) {
     std::call_once(g_encode_once, [] {
         void* fn = nullptr;
         cudaDriverEntryPointQueryResult q{};
@@ -1334,13 +1336,7 @@ bool find_encode() {
             q == cudaDriverEntryPointSuccess)
             g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
     });
-    return g_encode != nullptr;
-}
-
-// [rows][H][128] bf16 viewed as a 3-D tensor (channel, head, row); boxes of
-// 64 channels x 1 head x 16 rows, 128-byte swizzle (one 128-byte row per token)
-cudaError_t encode_rows(CUtensorMap* map, const void* base, int H, long long rows) {
-    if (!find_encode()) return cudaErrorNotSupported;
+    if (g_encode == nullptr) return cudaErrorNotSupported;
     const cuuint64_t dims[3] = {(cuuint64_t)kDim, (cuuint64_t)H, (cuuint64_t)rows};
     const cuuint64_t strides[2] = {(cuuint64_t)kDim * 2, (cuuint64_t)H * kDim * 2};
     const cuuint32_t box[3] = {64, 1, (cuuint32_t)kChunk};
@@ -1353,20 +1349,6 @@ cudaError_t encode_rows(CUtensorMap* map, const void* base, int H, long long row
 }
 
 }  // namespace
-
-cudaError_t encode_rows_map(CUtensorMap* map, const void* base, long long inner, long long rows,
-                            long long pitch, int box_rows) {
-    if (!find_encode()) return cudaErrorNotSupported;
-    const cuuint64_t dims[2] = {(cuuint64_t)inner, (cuuint64_t)rows};
-    const cuuint64_t strides[1] = {(cuuint64_t)pitch * 2};
-    const cuuint32_t box[2] = {64, (cuuint32_t)box_rows};
-    const cuuint32_t estr[2] = {1, 1};
-    const CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims,
-                                strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
-}
 
 size_t fused_smem_bytes() { return sizeof(Smem) + 1024; }
 

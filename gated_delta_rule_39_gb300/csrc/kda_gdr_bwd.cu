@@ -41,7 +41,11 @@ using namespace gdr;
 // (chunk, key head) pairs with a stride; a head's tiles are fetched while the one before is worked on, each
 // as soon as its place is free (without that, waiting for them took 40 % of the time).  With
 // fewer pairs than SMs (kSplit), a cluster shares a pair's value heads and adds dQ and dK up,
-// in the order of its CTAs.
+// in the order of its CTAs (512 tokens x 8 heads on 4 key heads: 15 us, 25 without).
+//
+// Measured: 4,096 tokens x 32 heads 147 us, 11 us per head and SM; 61 % of the cycles move shared
+// memory (operands of mma.sync, read again by every warp that needs them) and 0.37 of the issue
+// slots are taken.
 constexpr int kChunkThreads = 512, kParts = kChunkThreads / 128;
 
 constexpr int kPairBytes = kBlockUsed - kTileBytes;   // of a block, from P on

@@ -136,8 +136,6 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 }
 __device__ __forceinline__ float bf16_lo(uint32_t u) { return __uint_as_float(u << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t u) { return __uint_as_float(u & 0xFFFF0000u); }
-// two bf16 values as two fp16 ones (exact between 2^-14 and 65,504)
-__device__ __forceinline__ uint32_t bf16_to_half2(uint32_t u) { return pack_half2(bf16_lo(u), bf16_hi(u)); }
 // fp32 bits rounded to tf32 (nearest, ties away): the tensor core reads the top 19 bits
 __device__ __forceinline__ uint32_t tf32_bits(float x) { return __float_as_uint(x) + 0x1000u; }
 

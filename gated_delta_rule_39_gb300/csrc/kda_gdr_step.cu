@@ -7,7 +7,12 @@
 // its first read to its write: lane (rg, cq) = (lane / 4, lane % 4) holds rows rg + 8 i and
 // the 4 columns 4 cq ..  A token needs S'^T k and S'^T q, both from the decayed state
 // (o = scale (S'^T q + (k.q) d)), so its 9 sums over rows are one butterfly over the 8 row
-// groups and warps never wait for one another.  Everything is fp32.
+// groups, and warps share nothing but a token's keys and queries.  Everything is fp32.
+//
+// Measured: one token for 256 sequences x 96 heads 464 us, 7.0 TB/s (more than a plain copy's
+// 6.78).  Five tokens for 16 x 32 heads 19 us against a floor of 10: there the states stay in L2 on
+// their way out and the 1,024 CTAs' instructions (half of all issue slots) count.  Pairs of fp32
+// in one instruction (27 us) and keys straight from global memory (23) were no faster.
 #include "kda_gdr.cuh"
 
 namespace kda {

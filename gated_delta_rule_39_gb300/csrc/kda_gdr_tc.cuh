@@ -2,7 +2,7 @@
 // shared memory as tcgen05.mma reads them, products, and the hand-over between warps.
 #pragma once
 #include "kda_gdr_chunk.cuh"
-#include "kda_tcgen05.cuh"
+#include "kda_tcgen05_warp.cuh"
 
 namespace kda {
 namespace gdr {
@@ -18,7 +18,6 @@ __device__ __forceinline__ int rows_tile_at(int token, int unit) {   // byte of 
 }
 constexpr int kTokenRows = 8;             // tokens of a row tile that a producer thread holds
 constexpr int kProducers = 128;           // threads of a group: (token row0 + 8 i, unit)
-constexpr int kBlockSmem = (kBlockUsed + 1023) / 1024 * 1024;
 
 // Descriptors: K-major tiles start at their k-step's 32 bytes, 4 steps a block
 __device__ __forceinline__ uint64_t desc_k(uint32_t smem) { return tc::smem_desc(smem, 16, 1024, tc::kSwizzle128B); }

@@ -15,6 +15,10 @@
 // neighbours as pairs, 2 VEC consecutive channels.  So the rotation needs no exchange
 // between lanes and the sums over a row are a butterfly over its group.  Sums, the norm,
 // the rotation and the products are fp32; the result is rounded once, on the store.
+//
+// Measured (GB300, copy bandwidth 6.78 TB/s): 8,192 tokens x 72 heads x 128 bf16 with weights
+// and rotation 57 us, 5.3 TB/s, where issue slots (0.62 per cycle) begin to matter beside
+// memory; the same backwards 76 us; 16,384 x 64 heads backwards without either 121 us, 6.6 TB/s.
 #include <algorithm>
 #include <cmath>
 
@@ -29,7 +33,8 @@ __host__ __device__ constexpr int rows_at_once(int vec) { return vec > 1 ? 2 : 1
 constexpr int kManyHeads = 8;             // of a token, at most, for a group that reads its angles once
 constexpr int kFwdPerSm = 2;              // blocks of the forward pass
 // Blocks of the backward pass: three where 80 registers hold a lane's part (16-byte bf16
-// accesses, no angles, weights or their gradients), else two.
+// accesses, no angles, weights or their gradients: 16,384 x 64 heads 123 us, with two 141), else two
+// (with angles and weights three spill: 1,009 x 15 heads fp32 33 us, with two 15).
 __host__ __device__ constexpr int bwd_per_sm(int vec, bool more) { return vec == 8 && !more ? 3 : 2; }
 constexpr int kNormMaxDim = 512;
 
@@ -464,7 +469,8 @@ __global__ void __launch_bounds__(kDwThreads) qk_norm_dw_kernel(NormProblem P) {
 }
 
 // Calls f<T, VEC, NS>() for the widest access that the problem's sizes, strides and
-// addresses allow: 16 bytes, or single elements.
+// addresses allow: 16 bytes, or single elements (8,192 x 72 heads x 128 bf16: 56 against 228 us,
+// fp32 105 against 225).
 template <class F>
 cudaError_t with_width(const NormProblem& P, int dtype, bool wide, F&& f) {
     const int vec = !wide ? 1 : dtype == KDA_BF16 ? 8 : 4;
@@ -500,8 +506,9 @@ long long blocks_for(long long items, int lanes) {
     return (items + per_block - 1) / per_block;
 }
 
-// Heads of an item: as many as share angles and weights well, but a group keeps four items at
-// least, so that few rows are spread over all groups and the walk ends evenly.
+// Heads of an item: as many as share angles and weights well (8,192 x 72 heads: 8 for 2 at a time
+// 60 us, always 2 at a time 93), but a group keeps four items at least, so that few rows are
+// spread over all groups and the walk ends evenly (1,009 x 15 heads backwards: 1 for 8, 15 against 19 us).
 int item_heads(long long rows, int least, int lanes, int blocks) {
     const long long groups = (long long)blocks * (kNormThreads / lanes);
     int hb = least;

@@ -351,6 +351,9 @@ int kda_decode(const void* q, const void* k, const void* v, const void* g, const
  * asynchronous on `stream`, argument errors returned before anything is launched or
  * written.  Indices that only the device can check (positions, slots, lengths, tokens)
  * set KDA_ERR_BAD_INDEX in the error word, and what they belong to is not written.
+ * kda_gdr_fwd and kda_gdr_bwd give part of one long sequence's work to a stream of the
+ * library's own that waits for `stream` and that `stream` waits for (not while it is being
+ * captured); to the caller everything is on `stream`.
  */
 
 /*
