@@ -185,21 +185,23 @@ __device__ void issue(const GdrChunked& P, ChainSmem& S, int nch, uint32_t tmem)
         if (!wait(S.s16, turn)) return;
         product_k<8>(tmem + kTmAcc, s16, stage + offsetof(ChainSmem::Stage, kn), kId64, true, on);
         tc::commit_on(smem_u32(&S.acc), on);
+        // a wait takes 200 cycles even if it is over: each is where nothing waits for this warp
+        if (c + 1 < nch && !there(c + 1)) return;
+        if (!kSave && c >= 2 && !wait(S.o_free[turn], phase ^ 1u)) return;   // the outputs of chunk c - 2 have been read
         if (!wait(S.r16, turn)) return;
         product_k<4>(tmem + kTmAcc, tmem + kTmR16, stage + offsetof(ChainSmem::Stage, tp), kId64, false, on);
         tc::commit_on(smem_u32(&S.x), on);
-        if (c + 1 < nch && !there(c + 1)) return;
+        if (!kSave && !wait(S.q_full, turn)) return;
         if (!wait(S.x16, turn)) return;
         product_mn(tmem + kTmS, tmem + kTmX16, stage + offsetof(ChainSmem::Stage, kd), kId128, true, on);
         tc::commit_on(smem_u32(&S.s_done), on);
-        if (c + 1 < nch) begin(c + 1);
-        if (!kSave) {                         // outputs, once the queries are there and those of chunk c - 2 read
-            if (!wait(S.q_full, turn) || (c >= 2 && !wait(S.o_free[turn], phase ^ 1u))) return;
+        if (!kSave) {                         // outputs
             const uint32_t o = tmem + kTmO + 64 * uniform(turn);
             product_k<8>(o, s16, smem_u32(S.q), kId64, false, on);
             product_k<4>(o, tmem + kTmX16, stage + offsetof(ChainSmem::Stage, tp) + kTileBytes, kId64, true, on);
             tc::commit_on(smem_u32(&S.o_done[turn]), on);
         }
+        if (c + 1 < nch) begin(c + 1);
         tc::commit_on(smem_u32(&S.empty[c % kStages]), on);
     }
 }
