@@ -170,7 +170,8 @@ struct Fork {
 };
 
 // Prep and chain in two parts, the second's prep on a stream of its own beside the first's
-// chain; `carry` holds the fp32 states between the parts.
+// chain; `carry` holds the fp32 states between the parts.  (No kernel begins early here: the chains'
+// CTAs would hold SMs that prep could use, 8,192 tokens x 96 heads 358 us for 334.)
 cudaError_t run_in_parts(const GdrChunked& P, int first, float* carry, int sms, cudaStream_t s) {
     GdrChunked a = part_of(P, 0, first), b = part_of(P, first, P.chunks.total - first);
     a.final_state = carry;
@@ -178,10 +179,10 @@ cudaError_t run_in_parts(const GdrChunked& P, int first, float* carry, int sms, 
     b.init_state = carry;
     b.init_dtype = KDA_F32;
     const auto prep = [&](const GdrChunked& part, cudaStream_t on) {
-        return timed_launch(KDA_KERNEL_GDR_PREP, on, [&] { return launch_gdr_prep(part, sms, on); });
+        return timed_launch(KDA_KERNEL_GDR_PREP, on, [&] { return launch_gdr_prep(part, sms, false, on); });
     };
     const auto chain = [&](const GdrChunked& part) {
-        return timed_launch(KDA_KERNEL_GDR_CHAIN, s, [&] { return launch_gdr_chain(part, s); });
+        return timed_launch(KDA_KERNEL_GDR_CHAIN, s, [&] { return launch_gdr_chain(part, false, s); });
     };
     Fork fork(s);
     cudaError_t e = fork.make();
@@ -370,9 +371,9 @@ int kda_gdr_fwd(const void* q, const void* k, const void* v, const void* g, cons
     if (first_part) {
         e = run_in_parts(P, first_part, reinterpret_cast<float*>(scratch + block_bytes), sms, s);
     } else {
-        if (e == cudaSuccess) e = timed_launch(KDA_KERNEL_GDR_PREP, s, [&] { return launch_gdr_prep(P, sms, s); });
+        if (e == cudaSuccess) e = timed_launch(KDA_KERNEL_GDR_PREP, s, [&] { return launch_gdr_prep(P, sms, true, s); });
         if (e == cudaSuccess)
-            e = timed_launch(KDA_KERNEL_GDR_CHAIN, s, [&] { return launch_gdr_chain(P, s); });
+            e = timed_launch(KDA_KERNEL_GDR_CHAIN, s, [&] { return launch_gdr_chain(P, true, s); });
     }
     cudaFreeAsync(scratch, s);
     if (e != cudaSuccess) return cuda_fail(KDA_ERR_LAUNCH, e);

@@ -26,7 +26,6 @@
 // fixed order.
 #include <algorithm>
 
-#include "kda_cluster.cuh"
 #include "kda_gdr_chunk.cuh"
 
 namespace kda {
@@ -152,6 +151,7 @@ __device__ __forceinline__ void store_gate(void* p, int dtype, size_t i, float x
 template <bool kSplit>
 __global__ void __launch_bounds__(kChunkThreads, 1) gdr_bwd_chunk_kernel(GdrBackward B, int split) {
     extern __shared__ __align__(128) unsigned char raw[];
+    previous_done();
     ChunkSmem& S = *reinterpret_cast<ChunkSmem*>(raw);
     const GdrChunked& P = B.fwd;
     const GdrInputs& I = P.in;
@@ -564,8 +564,7 @@ cudaError_t launch_gdr_bwd_chunk(const GdrBackward& B, int sms, cudaStream_t s) 
     }
     const cudaError_t e = allow_smem<gdr_bwd_chunk_kernel<false>>(sizeof(ChunkSmem));
     if (e != cudaSuccess) return e;
-    gdr_bwd_chunk_kernel<false><<<(unsigned)std::min<long long>(pairs, sms), kChunkThreads, sizeof(ChunkSmem), s>>>(B, 1);
-    return cudaGetLastError();
+    return launch_after(true, gdr_bwd_chunk_kernel<false>, dim3((unsigned)std::min<long long>(pairs, sms)), kChunkThreads, sizeof(ChunkSmem), s, B, 1);
 }
 
 }  // namespace kda

@@ -345,6 +345,7 @@ static_assert(kBackThreads == chain::kChainThreads, "one launch for both chains"
 // sequence's time is the longer one's, not the sum.  The longer ones, the gradient's, come first.
 __global__ void __launch_bounds__(kBackThreads, 1) gdr_bwd_chain_kernel(GdrBackward B, GdrChunked F, const __grid_constant__ CUtensorMap vmap) {
     extern __shared__ __align__(1024) unsigned char raw[];
+    previous_done();
     const GdrInputs& I = B.fwd.in;
     if (I.cu && !*I.valid) return;
     const int units = I.N * I.Hv, unit = blockIdx.x % units, n = sequence_of(B.fwd.chunks, unit / I.Hv), h = unit % I.Hv;
@@ -362,8 +363,8 @@ cudaError_t launch_gdr_bwd_chain(const GdrBackward& B, const GdrChunked* states_
     cudaError_t e = allow_smem<gdr_bwd_chain_kernel>(smem);
     if (e == cudaSuccess && states_too) e = chain::values_map(*states_too, &vmap);
     if (e != cudaSuccess) return e;
-    gdr_bwd_chain_kernel<<<(unsigned)(states_too ? 2 * units : units), kBackThreads, smem, s>>>(B, states_too ? *states_too : B.fwd, vmap);
-    return cudaGetLastError();
+    return launch_after(true, gdr_bwd_chain_kernel, dim3((unsigned)(states_too ? 2 * units : units)), kBackThreads, smem, s, B,
+                        states_too ? *states_too : B.fwd, vmap);
 }
 
 }  // namespace kda

@@ -19,6 +19,7 @@
 // operands gave 3e-3; its price is that keys, queries, values and states have to stay
 // below 65,504.  The inverse T is formed in fp32 with tf32 products between its blocks.
 #pragma once
+#include "kda_cluster.cuh"
 #include "kda_gdr.cuh"
 
 #ifndef KDA_WAIT_TRIES
@@ -220,8 +221,9 @@ cudaError_t launch_gdr_bwd_chain(const GdrBackward& P, const GdrChunked* states_
 // on `sms` SMs
 cudaError_t launch_gdr_bwd_chunk(const GdrBackward& P, int sms, cudaStream_t s);
 cudaError_t launch_gdr_map(const GdrInputs& in, int* first, int* order, int* valid, int* err, cudaStream_t s);
-cudaError_t launch_gdr_prep(const GdrChunked& P, int sms, cudaStream_t s);
+// `early`: may begin before the kernel before it has ended
+cudaError_t launch_gdr_prep(const GdrChunked& P, int sms, bool early, cudaStream_t s);
 cudaError_t launch_gdr_prep(const GdrBackward& P, int sms, cudaStream_t s);   // finds the largest gradients too
-cudaError_t launch_gdr_chain(const GdrChunked& P, cudaStream_t s);
+cudaError_t launch_gdr_chain(const GdrChunked& P, bool early, cudaStream_t s);
 
 }  // namespace kda

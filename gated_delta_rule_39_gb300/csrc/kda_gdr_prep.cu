@@ -24,6 +24,7 @@ __global__ void __launch_bounds__(kMapThreads) gdr_map_kernel(GdrInputs I, int* 
     __shared__ int sums[kMapThreads / 32];
     __shared__ int places[kBuckets];
     __shared__ int bad;
+    next_may_begin();
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
     if (tid == 0) bad = I.cu[0] != 0 || I.cu[I.N] != I.T;
     if (tid < kBuckets) places[tid] = 0;
@@ -232,6 +233,8 @@ template <bool kGrads, bool kSplit>
 __global__ void __launch_bounds__(kPrepThreads, kPrepPerSm) gdr_prep_kernel(GdrChunked P, GdrGrads B, int ways) {
     const int split = kSplit ? ways : 1;
     extern __shared__ __align__(128) unsigned char raw[];
+    next_may_begin();
+    previous_done();
     PrepSmem& S = *reinterpret_cast<PrepSmem*>(raw);
     const GdrInputs& I = P.in;
     const int tid = threadIdx.x, lane = tid & 31, g = lane >> 2, t = lane & 3;
@@ -435,24 +438,23 @@ cudaError_t launch_gdr_map(const GdrInputs& in, int* first, int* order, int* val
 }
 
 template <bool kGrads, bool kSplit>
-static cudaError_t launch_prep(const GdrChunked& P, const GdrGrads& B, int split, cudaStream_t s) {
+static cudaError_t launch_prep(const GdrChunked& P, const GdrGrads& B, int split, bool early, cudaStream_t s) {
     const cudaError_t e = allow_smem<gdr_prep_kernel<kGrads, kSplit>>(sizeof(PrepSmem));
     if (e != cudaSuccess) return e;
-    gdr_prep_kernel<kGrads, kSplit><<<dim3(P.chunks.total, P.in.Hk * split), kPrepThreads, sizeof(PrepSmem), s>>>(P, B, split);
-    return cudaGetLastError();
+    return launch_after(early, gdr_prep_kernel<kGrads, kSplit>, dim3(P.chunks.total, P.in.Hk * split), kPrepThreads, sizeof(PrepSmem), s, P, B, split);
 }
 template <bool kGrads>
-static cudaError_t launch_prep(const GdrChunked& P, const GdrGrads& B, int sms, cudaStream_t s) {
+static cudaError_t launch_prep(const GdrChunked& P, const GdrGrads& B, int sms, bool early, cudaStream_t s) {
     if (P.chunks.total == 0) return cudaSuccess;
     const int share = P.in.Hv / P.in.Hk;
     int split = 1;
     while (2 * split <= share && (long long)P.chunks.total * P.in.Hk * 2 * split <= (long long)kPrepPerSm * sms &&
            P.in.Hk * 2 * split <= 65535)
         split *= 2;
-    return split > 1 ? launch_prep<kGrads, true>(P, B, split, s) : launch_prep<kGrads, false>(P, B, 1, s);
+    return split > 1 ? launch_prep<kGrads, true>(P, B, split, early, s) : launch_prep<kGrads, false>(P, B, 1, early, s);
 }
 
-cudaError_t launch_gdr_prep(const GdrChunked& P, int sms, cudaStream_t s) { return launch_prep<false>(P, {}, sms, s); }
-cudaError_t launch_gdr_prep(const GdrBackward& B, int sms, cudaStream_t s) { return launch_prep<true>(B.fwd, B.in, sms, s); }
+cudaError_t launch_gdr_prep(const GdrChunked& P, int sms, bool early, cudaStream_t s) { return launch_prep<false>(P, {}, sms, early, s); }
+cudaError_t launch_gdr_prep(const GdrBackward& B, int sms, cudaStream_t s) { return launch_prep<true>(B.fwd, B.in, sms, true, s); }
 
 }  // namespace kda
