@@ -20,6 +20,7 @@ namespace {
 
 constexpr int kStepThreads = 128;          // 4 warps: 64 columns
 constexpr int kStepCols = 16;              // columns of a warp
+constexpr int kStepParts = kDim / (kStepCols * kStepThreads / 32);   // CTAs of a state, next to one another
 constexpr int kRowGroups = 8;
 constexpr int kStepRows = kDim / kRowGroups;
 
@@ -43,8 +44,8 @@ __global__ void __launch_bounds__(kStepThreads) gdr_step_kernel(GdrStep P) {
     const GdrInputs& I = P.in;
     if (I.cu && !*I.valid) return;
     const int tid = threadIdx.x, lane = tid & 31, rg = lane >> 2, cq = lane & 3;
-    const int h = blockIdx.x % I.Hv, n = blockIdx.x / I.Hv;
-    const int col = blockIdx.y * (kStepThreads / 32) * kStepCols + (tid >> 5) * kStepCols + 4 * cq;
+    const int unit = blockIdx.x / kStepParts, h = unit % I.Hv, n = unit / I.Hv;
+    const int col = blockIdx.x % kStepParts * (kStepThreads / 32) * kStepCols + (tid >> 5) * kStepCols + 4 * cq;
     const long long start = I.cu ? I.cu[n] : (long long)n * I.T;
     const int len = I.cu ? I.cu[n + 1] - I.cu[n] : I.T;
     const int slot = P.slots ? P.slots[n] : n;
@@ -132,8 +133,7 @@ __global__ void __launch_bounds__(kStepThreads) gdr_step_kernel(GdrStep P) {
 cudaError_t launch_gdr_step(const GdrStep& P, cudaStream_t s) {
     const long long units = (long long)P.in.N * P.in.Hv;
     if (units == 0) return cudaSuccess;
-    const dim3 grid((unsigned)units, kDim / (kStepCols * kStepThreads / 32));
-    gdr_step_kernel<<<grid, kStepThreads, 0, s>>>(P);
+    gdr_step_kernel<<<(unsigned)(units * kStepParts), kStepThreads, 0, s>>>(P);
     return cudaGetLastError();
 }
 
