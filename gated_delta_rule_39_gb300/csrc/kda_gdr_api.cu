@@ -108,17 +108,23 @@ cudaError_t side_stream(cudaStream_t* out) {
     return cudaSuccess;
 }
 
+// Whether a stream is being captured into a graph (or cannot say: then it is not forked either).
+bool capturing(cudaStream_t s) {
+    cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+    if (cudaStreamIsCapturing(s, &capture) == cudaSuccess) return capture != cudaStreamCaptureStatusNone;
+    cudaGetLastError();                    // not a fault of the call
+    return true;
+}
+
 // How many chunks of one long sequence to prepare before its chains begin; the rest are prepared
 // beside them, on the SMs that the chains (one per value head) leave.  0: not worth it, or the stream is
 // being captured.  A chain takes 1.6 us per chunk and the whole GPU 0.0122 us to prepare a chunk of a
 // head, so while a chain walks a chunk the idle SMs prepare `rate` of them; of two parts the first is 1
-// in 1 + rate.  (8,192 tokens: 96 heads 359 -> 337 us, 64 heads 303 -> 273, 32
-// heads 240 -> 225.)
+// in 1 + rate.  (8,192 tokens: 96 heads 359 -> 337 us, 64 heads 303 -> 273, 32 heads 240 -> 225.)
 int chunks_before(const GdrChunked& P, int sms, cudaStream_t s) {
     const int units = P.in.Hv, chunks = P.chunks.total;
     if (P.in.cu || P.in.N != 1 || chunks < 64 || (long long)chunks * units < 2500 || units >= sms - sms / 8) return 0;
-    cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
-    if (cudaStreamIsCapturing(s, &capture) != cudaSuccess || capture != cudaStreamCaptureStatusNone) return 0;
+    if (capturing(s)) return 0;
     const float rate = 1.6f / 0.0122f * (float)(sms - units) / ((float)units * (float)sms);
     return std::max(8, (int)std::ceil((float)chunks / (1.0f + rate)));
 }
@@ -211,8 +217,7 @@ bool in_two_parts(const GdrInputs& in, int chunks, int sms) {
 int chunks_first(const GdrBackward& B, int sms, cudaStream_t s) {
     const int units = B.fwd.in.Hv, chunks = B.fwd.chunks.total;
     if (!in_two_parts(B.fwd.in, chunks, sms)) return 0;
-    cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
-    if (cudaStreamIsCapturing(s, &capture) != cudaSuccess || capture != cudaStreamCaptureStatusNone) return 0;
+    if (capturing(s)) return 0;
     const float rate = 0.073f / 2.4f * (float)units * (float)sms / (float)(sms - units);
     return std::min(chunks - 1, (int)((float)chunks * std::max(1.6f / 2.4f, 1.0f / (1.0f + rate))));
 }
