@@ -31,11 +31,14 @@ constexpr int kNormThreads = 256;
 // Heads that a group of the forward pass holds at a time: as many as 128 registers have room for.
 __host__ __device__ constexpr int rows_at_once(int vec) { return vec > 1 ? 2 : 1; }
 constexpr int kManyHeads = 8;             // of a token, at most, for a group that reads its angles once
-constexpr int kFwdPerSm = 2;              // blocks of the forward pass
-// Blocks of the backward pass: three where 80 registers hold a lane's part (16-byte bf16
-// accesses, no angles, weights or their gradients: 16,384 x 64 heads 123 us, with two 141), else two
-// (with angles and weights three spill: 1,009 x 15 heads fp32 33 us, with two 15).
-__host__ __device__ constexpr int bwd_per_sm(int vec, bool more) { return vec == 8 && !more ? 3 : 2; }
+// Blocks per SM, by the registers that a lane's part takes (vec x ns channels of each half of a row;
+// angles, weights and the weights' gradients add as many each).  Forwards:
+__host__ __device__ constexpr int fwd_per_sm(int vec, int ns) { return vec * ns <= 2 ? 3 : 2; }
+// Backwards, three where 80 registers are enough (bf16, 16,384 x 64 heads without angles and weights 123
+// us, with two blocks 141); with angles and weights on 16-byte accesses three would spill.
+__host__ __device__ constexpr int bwd_per_sm(int vec, int ns, bool rot, bool w) {
+    return vec * ns <= 2 || (vec * ns <= 4 && !w) || (vec == 8 && !rot && !w) ? 3 : 2;
+}
 constexpr int kNormMaxDim = 512;
 
 struct NormSide {             // the queries' part of a call, or the keys'
@@ -212,7 +215,7 @@ __device__ __forceinline__ bool load_angles(const NormProblem& P, int t, int slo
 __host__ __device__ inline unsigned head_blocks(int heads, int hb) { return ((unsigned)heads + hb - 1) / hb; }
 
 template <typename T, int VEC, int NS>
-__global__ void __launch_bounds__(kNormThreads, kFwdPerSm) qk_norm_kernel(NormProblem P, int hb) {
+__global__ void __launch_bounds__(kNormThreads, fwd_per_sm(VEC, NS)) qk_norm_kernel(NormProblem P, int hb) {
     constexpr int R = rows_at_once(VEC);
     const unsigned per_warp = 32 / P.lanes;
     const int lane = threadIdx.x & 31, li = lane % P.lanes, slots = P.D / (2 * VEC);
@@ -313,7 +316,7 @@ __global__ void __launch_bounds__(kNormThreads, kFwdPerSm) qk_norm_kernel(NormPr
 // channels of dw over its rows, and the block writes one partial row of D sums (in a fixed order:
 // results do not depend on scheduling).
 template <typename T, int VEC, int NS, bool kRot, bool kW>
-__global__ void __launch_bounds__(kNormThreads, bwd_per_sm(VEC, kRot || kW)) qk_norm_bwd_kernel(NormProblem P, int hb) {
+__global__ void __launch_bounds__(kNormThreads, bwd_per_sm(VEC, NS, kRot, kW)) qk_norm_bwd_kernel(NormProblem P, int hb) {
     __shared__ __align__(16) float part[kW ? kNormThreads / 32 : 1][kNormMaxDim];
     const int side = blockIdx.x >= P.side[0].blocks, block = blockIdx.x - (side ? P.side[0].blocks : 0);
     const NormSide& S = P.side[side];
@@ -469,18 +472,20 @@ __global__ void __launch_bounds__(kDwThreads) qk_norm_dw_kernel(NormProblem P) {
 }
 
 // Calls f<T, VEC, NS>() for the widest access that the problem's sizes, strides and
-// addresses allow: 16 bytes, or single elements (8,192 x 72 heads x 128 bf16: 56 against 228 us,
-// fp32 105 against 225).
+// addresses allow: 16 bytes, or single elements (8,192 x 72 heads x 128 bf16: 56 against 128 us,
+// fp32 99 against 142).
+// NS slots per lane as a row needs them: a lane that could hold more has fewer registers for its rows
+// (8,192 x 72 heads x 128 fp32 backwards with weights and angles: 169 us, with two 245).
 template <class F>
 cudaError_t with_width(const NormProblem& P, int dtype, bool wide, F&& f) {
     const int vec = !wide ? 1 : dtype == KDA_BF16 ? 8 : 4;
     const int slots = P.D / (2 * vec);
     if (dtype == KDA_BF16) {
         if (wide) return f.template operator()<__nv_bfloat16, 8, 1>(slots);
-        return f.template operator()<__nv_bfloat16, 1, 8>(slots);
+        return slots <= 64 ? f.template operator()<__nv_bfloat16, 1, 2>(slots) : f.template operator()<__nv_bfloat16, 1, 8>(slots);
     }
-    if (wide) return f.template operator()<float, 4, 2>(slots);
-    return f.template operator()<float, 1, 8>(slots);
+    if (wide) return slots <= 32 ? f.template operator()<float, 4, 1>(slots) : f.template operator()<float, 4, 2>(slots);
+    return slots <= 64 ? f.template operator()<float, 1, 2>(slots) : f.template operator()<float, 1, 8>(slots);
 }
 
 bool wide_ok(const NormProblem& P, int dtype) {
@@ -523,7 +528,7 @@ struct LaunchFwd {
     template <typename T, int VEC, int NS>
     cudaError_t operator()(int slots) {
         P.lanes = group_lanes(slots);
-        const int room = kFwdPerSm * sms;
+        const int room = fwd_per_sm(VEC, NS) * sms;
         const int hb = item_heads((long long)P.T * (P.side[0].heads + P.side[1].heads), rows_at_once(VEC), P.lanes, room);
         const long long items = (long long)P.T * (head_blocks(P.side[0].heads, hb) + head_blocks(P.side[1].heads, hb));
         qk_norm_kernel<T, VEC, NS><<<(unsigned)std::min<long long>(room, blocks_for(items, P.lanes)), kNormThreads, 0, s>>>(P, hb);
@@ -537,7 +542,7 @@ struct LaunchBwd {
     // blocks between the sides by their rows, and no more than there are items for
     template <typename T, int VEC, int NS, bool kRot, bool kW>
     cudaError_t run() {
-        const int heads = P.side[0].heads + P.side[1].heads, room = bwd_per_sm(VEC, kRot || kW) * sms;
+        const int heads = P.side[0].heads + P.side[1].heads, room = bwd_per_sm(VEC, NS, kRot, kW) * sms;
         const int hb = item_heads((long long)P.T * heads, 1, P.lanes, room);
         for (NormSide& S : P.side)
             S.blocks = S.heads ? (int)std::max<long long>(1, std::min<long long>((long long)room * S.heads / heads,
