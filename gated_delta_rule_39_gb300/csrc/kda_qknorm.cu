@@ -18,7 +18,8 @@
 //
 // Measured (GB300, copy bandwidth 6.78 TB/s): 8,192 tokens x 72 heads x 128 bf16 with weights
 // and rotation 57 us, 5.3 TB/s, where issue slots (0.62 per cycle) begin to matter beside
-// memory; the same backwards 76 us; 16,384 x 64 heads backwards without either 121 us, 6.6 TB/s.
+// memory; the same backwards 100 us, 76 without either (6.0 TB/s); 16,384 x 64 heads backwards without
+// either 121 us, 6.6 TB/s.  fp32, 8,192 x 72 x 128: 100 us, backwards 169 (142 without weights).
 #include <algorithm>
 #include <cmath>
 
