@@ -208,6 +208,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1) gdr_bwd_chunk_kernel(GdrBack
         pair += gridDim.x;
         more = !kSplit && place(P, pair, next);
         const int hk = now.hk, rows = now.rows;
+        // blocks of 16 tokens that the chunk has; the warps of the others only keep their sums at zero
+        const int blocks = (rows + 15) / 16;
+        const bool mine = rw < blocks;
         const long long tok = now.tok;
         const float sigma = grad_scale(B.in.amax[(size_t)now.n * I.Hk + hk]), back = 1.0f / sigma;
         const uint32_t sk = smem_u32(S.k[kq]), sq = smem_u32(S.q[kq]);
@@ -243,7 +246,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) gdr_bwd_chunk_kernel(GdrBack
                 fetch_gates(then, then_h, turn ^ 1);
                 if (last) fetch_pair(next, kq ^ 1);
             }
-            if (h == h0) {         // K K^T, this warp's 16 rows and 16 columns
+            if (h == h0 && mine) { // K K^T, this warp's 16 rows and 16 columns
 #pragma unroll
                 for (int j = 0; j < 2; ++j) kk[j][0] = kk[j][1] = kk[j][2] = kk[j][3] = 0.0f;
 #pragma unroll
@@ -258,7 +261,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) gdr_bwd_chunk_kernel(GdrBack
             const float e0 = gate[kGateE + i0], e1 = gate[kGateE + i1];
             const float be0 = gate[kGateBe + i0], be1 = gate[kGateBe + i1];
             const float b0 = gate[kGateB + i0], b1 = gate[kGateB + i1];
-            {
+            if (mine) {
                 float yv0 = 0.0f, yv1 = 0.0f;
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
@@ -275,6 +278,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1) gdr_bwd_chunk_kernel(GdrBack
                 if (t == 0) {
                     S.yv[part][i0] = yv0; S.yv[part][i1] = yv1;
                 }
+            } else {
+                if (t == 0)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) S.row[r][part][i0] = S.row[r][part][i1] = 0.0f;
+                if (lane < 16) S.col[rw][16 * part + lane] = 0.0f;
             }
             // <S, dS>: the diagonal of S^T dS, rows 16 (w / 2) .. over half of the key channels
             {
@@ -293,7 +301,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) gdr_bwd_chunk_kernel(GdrBack
                 for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, o);
                 if (lane == 0) S.dot[w] = x;
             }
-            {
+            if (mine) {
                 // dO X^T and Y X^T: this warp's 16 rows, 16 columns
                 float dp[2][4], da[2][4];
 #pragma unroll
@@ -359,7 +367,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) gdr_bwd_chunk_kernel(GdrBack
                 stsm(a_addr<128>(sdb, 16 * rw, 2 * part, lane), fb[0][0], fb[0][1], fb[1][0], fb[1][1]);
             }
             // dO S^T and Y S^T: this warp's rows, 32 key channels, over 128 value channels
-            {
+            if (mine) {
                 float a[4][4], z[4][4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
@@ -404,7 +412,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) gdr_bwd_chunk_kernel(GdrBack
             __syncthreads();               // dP and dB are there; S, Y and dO have been read
             if (follows) fetch_first(then, then_h);
             // X dS^T
-            {
+            if (mine) {
                 float a[4][4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) a[j][0] = a[j][1] = a[j][2] = a[j][3] = 0.0f;
@@ -441,6 +449,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) gdr_bwd_chunk_kernel(GdrBack
             // dQ += dP K, dK += dP^T Q + dB K + dB^T K
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks) {
+                if (!mine || ks >= blocks) break;
                 uint32_t fpn[4], fbn[4], fpt[4], fbt[4];
                 if (ks <= rw) {            // rows reach tokens up to their own
                     ldsm(fpn, a_addr<128>(sdp, 16 * rw, 2 * ks, lane));
