@@ -87,9 +87,11 @@ BwdLayout bwd_layout(bool varlen, int B, int T, int Hk, int Hv, int N) {
     return L;
 }
 
-// Sequences (of fixed length) of no more tokens go through the token-by-token kernel, where a short
-// chunk's fixed costs do not arise.  32 heads, fp32 states in place: 8 sequences of 1 and 8 tokens 15 and
-// 17 us (in chunks 21 and 21), 256 of them 158 and 326 (451 and 473); with 12 tokens 22 for 21 and 448 for 507.
+// More (sequence, head) units than SMs, of fixed length and no more tokens than this, go through the
+// token-by-token kernel, where a short chunk's fixed costs (8 us a unit and SM) do not arise.  32 heads, fp32
+// states in place: 8 sequences of 1 and 8 tokens 15 and 17 us (in chunks 21 and 21), 256 of them 158 and 326
+// (451 and 473); with 12 tokens 22 for 21 and 448 for 507.  Fewer units (8: 15 for 21 us) stay with the
+// chunks, so that the last piece of a sequence given in pieces has the bits that it has in the whole.
 constexpr int kFewTokens = 8;
 
 // A second stream of this device, made once.
@@ -362,7 +364,7 @@ int kda_gdr_fwd(const void* q, const void* k, const void* v, const void* g, cons
     P.final_state = final_state;
     P.final_dtype = final_state_dtype;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (!varlen && T <= kFewTokens) {
+    if (!varlen && T <= kFewTokens && (long long)N * Hv > sms) {
         const GdrStep Q{P.in, P.out, initial_state, initial_state_dtype, final_state, final_state_dtype, nullptr, nullptr, N, P.err};
         const cudaError_t e = timed_launch(KDA_KERNEL_GDR_STEP, s, [&] { return launch_gdr_step(Q, s); });
         return e == cudaSuccess ? KDA_OK : cuda_fail(KDA_ERR_LAUNCH, e);

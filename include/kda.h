@@ -418,7 +418,8 @@ int kda_qk_norm_bwd(const void* q, const void* k, const void* dq_out, const void
  * The state is carried in fp32; the tensor-core products have fp16 operands, so q, k, v and
  * the states have to stay below 65,504 in magnitude.  Takes about 0.3 KB of scratch per
  * token and value head from the stream-ordered allocator.  Deterministic.  (Without
- * cu_seqlens, T <= 8 is computed token by token in fp32 and takes no scratch.)
+ * cu_seqlens, T <= 8 with more sequences times heads than the GPU has SMs is computed token
+ * by token in fp32 and takes no scratch.)
  */
 int kda_gdr_fwd(const void* q, const void* k, const void* v, const void* g, const void* beta,
                 int gate_dtype, float scale, void* out, const void* initial_state,
