@@ -133,11 +133,15 @@ __device__ __forceinline__ void slot_channels(int slot, int half, int inter, int
         u1 = 2 * first + VEC;
     }
 }
-// A slot's channels as they are in memory: two units.
+// A slot's channels as they are in memory: two units, read 16 bytes at a time at most (which is what
+// wide_ok asks of every address: a unit of 8 fp32 weights begins on 16 bytes, not on 32).
 template <typename T, int VEC>
-struct __align__(sizeof(T) * VEC) Unit {
+struct __align__(sizeof(T) * VEC < 16 ? sizeof(T) * VEC : 16) Unit {
     T v[VEC];
 };
+static_assert(alignof(Unit<float, 8>) == 16 && alignof(Unit<__nv_bfloat16, 8>) == 16 && alignof(Unit<float, 4>) == 16 &&
+                  alignof(Unit<float, 1>) == 4 && alignof(Unit<__nv_bfloat16, 1>) == 2,
+              "no access wider than the alignment that calls are checked for");
 template <typename T, int VEC>
 struct Raw {
     Unit<T, VEC> e0, e1;
