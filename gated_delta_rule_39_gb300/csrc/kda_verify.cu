@@ -99,12 +99,13 @@ __global__ void __launch_bounds__(kVerThreads, 2) verify_kernel(VerifyProblem P,
     const int n = blockIdx.x / split, tid = threadIdx.x, lane = tid & 31;
     const unsigned rank = cluster_rank();
     cluster_arrive();                          // all CTAs have begun before one writes to another
-    const int units = P.V / VEC, step = split * kVerThreads, begin = (int)rank * kVerThreads + tid;
+    // unsigned: a turn may end up to kUnits x step after the row's end, past 2^31 for the longest rows
+    const unsigned units = P.V / VEC, step = split * kVerThreads, begin = rank * kVerThreads + tid;
     using Noise = Unit<float, VEC>;
     using Prob = Unit<T, VEC>;
     const Noise* e = reinterpret_cast<const Noise*>(P.noise + (size_t)n * P.V);
     Noise ev[kUnits];
-    const auto noise = [&](int base) {
+    const auto noise = [&](unsigned base) {
 #pragma unroll
         for (int j = 0; j < kUnits; ++j)
             if (base + j * step < units) ev[j] = e[base + j * step];
@@ -125,11 +126,11 @@ __global__ void __launch_bounds__(kVerThreads, 2) verify_kernel(VerifyProblem P,
     float top = 0.0f;                          // best's score
     // a second round, on p itself, where the first finds nothing left (p nowhere above q)
     for (int round = 0; round < 2; ++round) {
-        for (int base = begin; base < units; base += kUnits * step) {
+        for (unsigned base = begin; base < units; base += kUnits * step) {
             Prob pv[kUnits], qv[kUnits];
 #pragma unroll
             for (int j = 0; j < kUnits; ++j) {
-                const int u = base + j * step;
+                const unsigned u = base + j * step;
                 if (u < units) {
                     pv[j] = p[u];
                     if (q && !round) qv[j] = q[u];
@@ -141,7 +142,7 @@ __global__ void __launch_bounds__(kVerThreads, 2) verify_kernel(VerifyProblem P,
                 if (base + j * step >= units) break;
 #pragma unroll
                 for (int i = 0; i < VEC; ++i) {
-                    const int v = (base + j * step) * VEC + i;
+                    const int v = (int)((base + j * step) * VEC + i);
                     float rest = prob(pv[j].v, i);
                     if (!round) rest -= q ? prob(qv[j].v, i) : v == sure ? 1.0f : 0.0f;
                     // the division only where the score may be above the thread's best: the product
