@@ -599,7 +599,9 @@ int validate_norm(const void* q, const void* k, const void* yq, const void* yk, 
         if (table_rows < 0 || (!pos && table_rows < T)) return KDA_ERR_SHAPE;
     }
     if (q_stride < (long long)Hq * D || (Hk && k_stride < (long long)Hk * D)) return KDA_ERR_SHAPE;
-    if ((long long)T * (Hq + Hk) >= (1LL << 32)) return KDA_ERR_SHAPE;
+    // items are counted in 32 bits, and a group's walk ends up to one stride (fewer than 2^18 items on
+    // any GPU of this kind) after the last of them
+    if ((long long)T * (Hq + Hk) >= (1LL << 32) - (1LL << 18)) return KDA_ERR_SHAPE;
     const size_t size = dtype == KDA_BF16 ? 2 : 4;
     for (const void* p : {q, k, yq, yk})
         if (reinterpret_cast<uintptr_t>(p) % size) return KDA_ERR_ALIGN;

@@ -375,6 +375,7 @@ int kda_decode(const void* q, const void* k, const void* v, const void* g, const
  *               position outside the table sets KDA_ERR_BAD_INDEX and that token's rows are
  *               not written
  *   interleaved 0: channel i pairs with i + rotary_dim / 2; else 2 i with 2 i + 1
+ *   T (Hq + Hk) below 2^32 - 2^18 (KDA_ERR_SHAPE)
  *
  * Arithmetic is fp32, rounded once on the store.  Any element alignment and stride is
  * accepted; 16-byte aligned rows with rotary_dim / 2 a multiple of 8 (bf16) or 4 (fp32)
