@@ -1,10 +1,10 @@
 // Host-side helpers shared by the C ABI's translation units (defined in kda_api.cu).
 #pragma once
-#include <atomic>
 #include <cstddef>
 #include <cstdint>
 
 #include "kda_internal.cuh"
+#include "kda_per_device.h"
 
 namespace kda {
 
@@ -51,17 +51,25 @@ inline bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
     return x < y + nb && y < x + na;
 }
 
-// Lets a kernel use more than 48 KB of dynamic shared memory (once per device).
+// Sets an attribute of a kernel on the current device, the first time that it is used there.
+template <auto Kernel, cudaFuncAttribute Attribute>
+cudaError_t set_once(int value) {
+    static OncePerDevice once;
+    int dev = 0;
+    const cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= kMaxDeviceIndex) return cudaErrorInvalidDevice;
+    return once(dev, [&] { return cudaFuncSetAttribute(Kernel, Attribute, value); });
+}
+// Lets a kernel use more than 48 KB of dynamic shared memory
 template <auto Kernel>
 cudaError_t allow_smem(size_t bytes) {
-    static std::atomic<bool> done[64];
-    int dev = 0;
-    cudaGetDevice(&dev);
-    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-    if (done[dev].load(std::memory_order_acquire)) return cudaSuccess;
-    const cudaError_t e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-    if (e == cudaSuccess) done[dev].store(true, std::memory_order_release);
-    return e;
+    return set_once<Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize>((int)bytes);
+}
+// Lets a kernel run in clusters of more than 8 CTAs
+template <auto Kernel>
+cudaError_t allow_large_clusters() {
+    return set_once<Kernel, cudaFuncAttributeNonPortableClusterSizeAllowed>(1);
 }
 
 inline bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }

@@ -182,9 +182,8 @@ __global__ void __launch_bounds__(kVerThreads, 2) verify_kernel(VerifyProblem P,
 
 template <typename T, int VEC>
 cudaError_t launch(const VerifyProblem& P, int split, cudaStream_t s) {
-    static const cudaError_t allowed =         // clusters of more than 8 CTAs
-        cudaFuncSetAttribute(verify_kernel<T, VEC>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (allowed != cudaSuccess) return allowed;
+    const cudaError_t e = allow_large_clusters<verify_kernel<T, VEC>>();
+    if (e != cudaSuccess) return e;
     return launch_clusters(verify_kernel<T, VEC>, (unsigned)(P.N * split), kVerThreads, 0, (unsigned)split, s, P, split);
 }
 
