@@ -346,13 +346,12 @@ def kda_bwd(q, k, v, g, beta, scale: float, A_log, dt_bias, lower_bound: float, 
                                 cu_seqlens, dev)
     if d_final_state is not None:
         _check(d_final_state, "d_final_state", torch.float32, (N, H, K, V), dev)
-    f32 = dict(dtype=torch.float32, device=dev)
-    r = {"dq": torch.empty((B, T, H, K), **f32), "dk": torch.empty((B, T, H, K), **f32),
-         "dv": torch.empty((B, T, H, V), **f32), "dg": torch.empty((B, T, H, K), **f32),
-         "dbeta": torch.empty((B, T, H), **f32), "dA_log": torch.empty((H,), **f32),
-         "ddt_bias": torch.empty((H, K), **f32)}
+    shapes = {"dq": (B, T, H, K), "dk": (B, T, H, K), "dv": (B, T, H, V), "dg": (B, T, H, K),
+              "dbeta": (B, T, H), "dA_log": (H,), "ddt_bias": (H, K)}
     if d_initial_state:
-        r["d_initial_state"] = torch.empty((N, H, K, V), **f32)
+        shapes["d_initial_state"] = (N, H, K, V)
+    r = _operators.results_on(stream, dev, lambda: {
+        n: torch.empty(shape, dtype=torch.float32, device=dev) for n, shape in shapes.items()})
     if stream is None:
         stream = torch.cuda.current_stream(dev)
     s = ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))

@@ -55,6 +55,27 @@ def _call(name, device, stream, *args):
         raise kda.KdaError(rc, name)
 
 
+def results_on(stream, device, make):
+    """The tensors that ``make()`` allocates for a call on `stream` (a torch stream or a
+    handle; None: the current one) to write.  They come from that stream's memory, since what the
+    current stream's pool hands out may still be read or written by work queued there; and
+    memory that the current stream's work reads is not given away before that work is done."""
+    torch = _torch()
+    if stream is None:
+        return make()
+    if not hasattr(stream, "cuda_stream"):      # a handle; 0 and 1 are the default stream's
+        handle = int(stream)
+        stream = torch.cuda.ExternalStream(handle, device=device) if handle > 1 else torch.cuda.default_stream(device)
+    current = torch.cuda.current_stream(device)
+    if stream.cuda_stream == current.cuda_stream:
+        return make()
+    with torch.cuda.stream(stream):
+        r = make()
+    for t in r.values():
+        t.record_stream(current)
+    return r
+
+
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
@@ -172,11 +193,8 @@ def kda_qk_norm_bwd(q, k, dq_out, dk_out, norm: str = "l2", eps: float = 1e-6, q
                                           positions)
     _dense(dq_out, "dq_out", (q.dtype,), q.shape, dev)
     _dense(dk_out, "dk_out", (q.dtype,), k.shape, dev)
-    r = {"dq": torch.empty_like(dq_out), "dk": torch.empty_like(dk_out)}
-    if q_weight is not None:
-        r["dq_weight"] = torch.empty_like(q_weight)
-    if k_weight is not None:
-        r["dk_weight"] = torch.empty_like(k_weight)
+    like = {"dq": dq_out, "dk": dk_out, "dq_weight": q_weight, "dk_weight": k_weight}
+    r = results_on(stream, dev, lambda: {n: torch.empty_like(t) for n, t in like.items() if t is not None})
     _call("kda_qk_norm_bwd", dev, stream, _ptr(q), _ptr(k), _ptr(dq_out), _ptr(dk_out),
           _ptr(r["dq"]), _ptr(r["dk"]), f32, _NORMS[norm], eps, *w, _ptr(r.get("dq_weight")),
           _ptr(r.get("dk_weight")), *turn, int(interleaved), *sizes)
@@ -260,11 +278,11 @@ def kda_gdr_bwd(q, k, v, g, beta, scale: float, d_out, initial_state=None, d_fin
     N, num = _sequences(cu_seqlens, B, dev)
     states = _states(dev, (N, Hv, K, V), initial_state=initial_state, d_final_state=d_final_state)
     dense = torch.contiguous_format
-    r = {"dq": torch.empty_like(q, memory_format=dense), "dk": torch.empty_like(k, memory_format=dense),
-         "dv": torch.empty_like(d_out), "dg": torch.empty_like(g), "dbeta": torch.empty_like(beta)}
-    ds = None
+    like = {"dq": q, "dk": k, "dv": d_out, "dg": g, "dbeta": beta}
     if d_initial_state and initial_state is not None:
-        ds = r["d_initial_state"] = torch.empty_like(initial_state)
+        like["d_initial_state"] = initial_state
+    r = results_on(stream, dev, lambda: {n: torch.empty_like(t, memory_format=dense) for n, t in like.items()})
+    ds = r.get("d_initial_state")
     _call("kda_gdr_bwd", dev, stream, *head, scale, *states[:2], _ptr(d_out), *states[2:],
           _ptr(r["dq"]), _ptr(r["dk"]), _ptr(r["dv"]), _ptr(r["dg"]), _ptr(r["dbeta"]), _ptr(ds),
           int(ds is not None and ds.dtype == torch.float32), _ptr(cu_seqlens), num, B, T, Hk, Hv, K, V,
