@@ -1,8 +1,10 @@
 // The C entry points of the gated delta rule with one decay per value head: checks,
 // scratch and launches (the operation and its kernels: kda_gdr.cuh).
 #include <algorithm>
-#include <atomic>
 #include <cmath>
+#include <memory>
+#include <mutex>
+#include <vector>
 
 #include "kda_gdr_chunk.cuh"
 
@@ -94,24 +96,45 @@ BwdLayout bwd_layout(bool varlen, int B, int T, int Hk, int Hv, int N) {
 // chunks, so that the last piece of a sequence given in pieces has the bits that it has in the whole.
 constexpr int kFewTokens = 8;
 
-// A second stream of this device, made once.
-cudaError_t side_stream(cudaStream_t* out) {
-    static std::atomic<cudaStream_t> made[64];
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-    cudaStream_t s = made[dev].load(std::memory_order_acquire);
-    if (!s) {
-        e = cudaStreamCreateWithFlags(&s, cudaStreamNonBlocking);
-        if (e != cudaSuccess) return e;
-        cudaStream_t none = nullptr;
-        if (!made[dev].compare_exchange_strong(none, s)) {     // another thread was first
-            cudaStreamDestroy(s);
-            s = none;
-        }
+// A second stream for the calls on `s`, of its priority: one for each of the caller's streams, so that
+// calls on streams that do not depend on each other do not wait for each other there.  The streams
+// used last are kept (making one takes longer than a launch); one that falls out ends with its work.
+struct SideStream {
+    int device = -1;
+    unsigned long long of = 0;             // the caller's stream: an id that is never used again
+    cudaStream_t stream = nullptr;
+    SideStream() = default;
+    SideStream(const SideStream&) = delete;
+    SideStream& operator=(const SideStream&) = delete;
+    ~SideStream() {
+        if (stream) cudaStreamDestroy(stream);
     }
-    *out = s;
+};
+constexpr size_t kSideStreams = 32;
+
+cudaError_t side_stream(cudaStream_t s, std::shared_ptr<SideStream>* out) {
+    static std::mutex mu;
+    // last used first; never destroyed, since the driver may be gone by the time that statics are
+    static auto& kept = *new std::vector<std::shared_ptr<SideStream>>;
+    int dev = 0, priority = 0;
+    unsigned long long id = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaStreamGetId(s, &id);
+    if (e == cudaSuccess) e = cudaStreamGetPriority(s, &priority);
+    if (e != cudaSuccess) return e;
+    std::lock_guard<std::mutex> lock(mu);
+    auto at = std::find_if(kept.begin(), kept.end(), [&](const auto& x) { return x->device == dev && x->of == id; });
+    if (at == kept.end()) {
+        auto made = std::make_shared<SideStream>();
+        made->device = dev;
+        made->of = id;
+        e = cudaStreamCreateWithPriority(&made->stream, cudaStreamNonBlocking, priority);
+        if (e != cudaSuccess) return e;
+        if (kept.size() == kSideStreams) kept.pop_back();      // a call that still has it keeps it
+        at = kept.insert(kept.end(), std::move(made));
+    }
+    std::rotate(kept.begin(), at, at + 1);
+    *out = kept.front();
     return cudaSuccess;
 }
 
@@ -161,11 +184,13 @@ GdrChunked part_of(const GdrChunked& P, int first, int count) {
 
 // Two streams' work between two events: the second one joins the caller's again whatever happens.
 struct Fork {
+    std::shared_ptr<SideStream> kept;
     cudaStream_t s, side = nullptr;
     cudaEvent_t begun = nullptr, over = nullptr;
     explicit Fork(cudaStream_t s_) : s(s_) {}
     cudaError_t make() {
-        cudaError_t e = side_stream(&side);
+        cudaError_t e = side_stream(s, &kept);
+        if (e == cudaSuccess) side = kept->stream;
         if (e == cudaSuccess) e = cudaEventCreateWithFlags(&begun, cudaEventDisableTiming);
         if (e == cudaSuccess) e = cudaEventCreateWithFlags(&over, cudaEventDisableTiming);
         return e;

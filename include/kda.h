@@ -353,7 +353,8 @@ int kda_decode(const void* q, const void* k, const void* v, const void* g, const
  * set KDA_ERR_BAD_INDEX in the error word, and what they belong to is not written.
  * kda_gdr_fwd and kda_gdr_bwd give part of one long sequence's work to a stream of the
  * library's own that waits for `stream` and that `stream` waits for (not while it is being
- * captured); to the caller everything is on `stream`.
+ * captured); to the caller everything is on `stream`.  Each of the caller's streams has one of its
+ * own, of the same priority, so that calls on independent streams stay independent.
  */
 
 /*
