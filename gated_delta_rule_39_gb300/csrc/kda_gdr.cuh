@@ -22,7 +22,7 @@ struct GdrInputs {
 };
 
 struct GdrStep {          // the token-by-token kernel (kda_gdr_step.cu)
-    GdrInputs in;
+    GdrInputs in;         // N sequences of T (no cu)
     __nv_bfloat16* out;   // [tokens][Hv][128] or nullptr
     const void* state_in; // [pool][Hv][128][128] or nullptr (zero)
     int in_dtype;

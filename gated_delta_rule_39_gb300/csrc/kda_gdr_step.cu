@@ -42,12 +42,11 @@ __device__ __forceinline__ void store4(void* base, int dtype, size_t i, float4 x
 __global__ void __launch_bounds__(kStepThreads) gdr_step_kernel(GdrStep P) {
     __shared__ float s_k[2][kDim], s_q[2][kDim];
     const GdrInputs& I = P.in;
-    if (I.cu && !*I.valid) return;
     const int tid = threadIdx.x, lane = tid & 31, rg = lane >> 2, cq = lane & 3;
     const int unit = blockIdx.x / kStepParts, h = unit % I.Hv, n = unit / I.Hv;
     const int col = blockIdx.x % kStepParts * (kStepThreads / 32) * kStepCols + (tid >> 5) * kStepCols + 4 * cq;
-    const long long start = I.cu ? I.cu[n] : (long long)n * I.T;
-    const int len = I.cu ? I.cu[n + 1] - I.cu[n] : I.T;
+    const long long start = (long long)n * I.T;
+    const int len = I.T;
     const int slot = P.slots ? P.slots[n] : n;
     const int keep = P.lengths ? P.lengths[n] : len;
     if (slot == -1) return;                      // a padding entry
