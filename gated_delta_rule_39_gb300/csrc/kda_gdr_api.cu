@@ -276,8 +276,9 @@ cudaError_t run_backward(const GdrBackward& B, int last, float* carry, int sms, 
     const auto chain = [&](const GdrBackward& part, const GdrChunked* states_too) {
         return timed_launch(KDA_KERNEL_GDR_BWD_CHAIN, s, [&] { return launch_gdr_bwd_chain(part, states_too, s); });
     };
+    const int split = gdr_bwd_chunk_split(B, sms);
     const auto chunk = [&](const GdrBackward& part, int on_sms, cudaStream_t on) {
-        return timed_launch(KDA_KERNEL_GDR_BWD_CHUNK, on, [&] { return launch_gdr_bwd_chunk(part, on_sms, on); });
+        return timed_launch(KDA_KERNEL_GDR_BWD_CHUNK, on, [&] { return launch_gdr_bwd_chunk(part, split, on_sms, on); });
     };
     if (!last) {
         const cudaError_t e = chain(B, &B.fwd);

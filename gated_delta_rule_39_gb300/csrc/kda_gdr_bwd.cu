@@ -559,12 +559,17 @@ __global__ void __launch_bounds__(kChunkThreads, 1) gdr_bwd_chunk_kernel(GdrBack
 
 }  // namespace
 
-cudaError_t launch_gdr_bwd_chunk(const GdrBackward& B, int sms, cudaStream_t s) {
-    if (B.fwd.chunks.total == 0) return cudaSuccess;
+int gdr_bwd_chunk_split(const GdrBackward& B, int sms) {
     const long long pairs = (long long)B.fwd.chunks.total * B.fwd.in.Hk;
     const int share = B.fwd.in.Hv / B.fwd.in.Hk;
     int split = 1;                         // at most 8 CTAs, as many as there are heads and SMs for
     while (split < 8 && 2 * split <= share && pairs * 2 * split <= sms) split *= 2;
+    return split;
+}
+
+cudaError_t launch_gdr_bwd_chunk(const GdrBackward& B, int split, int sms, cudaStream_t s) {
+    if (B.fwd.chunks.total == 0) return cudaSuccess;
+    const long long pairs = (long long)B.fwd.chunks.total * B.fwd.in.Hk;
     if (split > 1) {
         const cudaError_t e = allow_smem<gdr_bwd_chunk_kernel<true>>(sizeof(ChunkSmem));
         if (e != cudaSuccess) return e;

@@ -218,8 +218,11 @@ struct GdrBackward {      // what the backward pass has besides
 
 // the gradient's chain, and with it the one that computes the states of `states_too` again (or nullptr)
 cudaError_t launch_gdr_bwd_chain(const GdrBackward& P, const GdrChunked* states_too, cudaStream_t s);
-// on `sms` SMs
-cudaError_t launch_gdr_bwd_chunk(const GdrBackward& P, int sms, cudaStream_t s);
+// on `sms` SMs, with `split` CTAs (a cluster) to a (chunk, key head) pair
+cudaError_t launch_gdr_bwd_chunk(const GdrBackward& P, int split, int sms, cudaStream_t s);
+// as many as the whole call has room for; its parts take the same, since the order in which a
+// group's heads are added up depends on it
+int gdr_bwd_chunk_split(const GdrBackward& P, int sms);
 cudaError_t launch_gdr_map(const GdrInputs& in, int* first, int* order, int* valid, int* err, cudaStream_t s);
 // `early`: may begin before the kernel before it has ended
 cudaError_t launch_gdr_prep(const GdrChunked& P, int sms, bool early, cudaStream_t s);
