@@ -93,7 +93,9 @@ BwdLayout bwd_layout(bool varlen, int B, int T, int Hk, int Hv, int N) {
 // token-by-token kernel, where a short chunk's fixed costs (8 us a unit and SM) do not arise.  32 heads, fp32
 // states in place: 8 sequences of 1 and 8 tokens 15 and 17 us (in chunks 21 and 21), 256 of them 158 and 326
 // (451 and 473); with 12 tokens 22 for 21 and 448 for 507.  Fewer units (8: 15 for 21 us) stay with the
-// chunks, so that the last piece of a sequence given in pieces has the bits that it has in the whole.
+// chunks.  Its arithmetic is fp32 where the chunks' operands are fp16, so the last bits of a short call
+// depend on which side of the rule its number of units is: one sequence's last piece has the bits that it has
+// in the whole only where its heads are no more than the SMs.
 constexpr int kFewTokens = 8;
 
 // A second stream for the calls on `s`, of its priority: one for each of the caller's streams, so that
