@@ -68,17 +68,16 @@ size_t plan_chunks(bool varlen, int B, int T, int N, gdr::Chunks* c) {
 
 constexpr int kPartUnits = 1000;          // chunks x heads from which a backward pass is done in two parts
 
-// Scratch of a backward pass (bytes from its start): the map of packed sequences, the
-// largest gradients, states between two parts, and per (chunk, value head) a block, T, S^T, X^T, dS^T and Y^T.
+// Scratch of a backward pass (bytes from its start): the map of packed sequences, states
+// between two parts, and per (chunk, value head) a block, T, S^T, X^T, dS^T and Y^T.
 struct BwdLayout {
     gdr::Chunks chunks{};
-    size_t amax, carry, blocks, ts, states, xs, dstates, ys, total;
+    size_t carry, blocks, ts, states, xs, dstates, ys, total;
 };
-BwdLayout bwd_layout(bool varlen, int B, int T, int Hk, int Hv, int N) {
+BwdLayout bwd_layout(bool varlen, int B, int T, int Hv, int N) {
     BwdLayout L{};
-    L.amax = plan_chunks(varlen, B, T, N, &L.chunks);
+    L.carry = plan_chunks(varlen, B, T, N, &L.chunks);
     const size_t units = (size_t)L.chunks.total * Hv;
-    L.carry = L.amax + align_up((size_t)N * Hk * 4);
     L.blocks = L.carry + (N == 1 && (long long)L.chunks.total * Hv >= kPartUnits ? align_up(state_bytes(1, Hv, KDA_F32)) : 0);
     L.ts = L.blocks + units * gdr::kBlockBytes;
     L.states = L.ts + units * gdr::kTileBytes;
@@ -427,7 +426,7 @@ int kda_gdr_fwd(const void* q, const void* k, const void* v, const void* g, cons
 
 size_t kda_gdr_bwd_workspace_bytes(int B, int T, int Hk, int Hv, int num_seqs, int varlen) {
     if (B < 1 || T < 0 || Hk < 1 || Hv < 1 || (varlen && num_seqs < 1)) return 0;
-    return bwd_layout(varlen != 0, B, T, Hk, Hv, varlen ? num_seqs : B).total;
+    return bwd_layout(varlen != 0, B, T, Hv, varlen ? num_seqs : B).total;
 }
 
 int kda_gdr_bwd(const void* q, const void* k, const void* v, const void* g, const void* beta,
@@ -475,7 +474,7 @@ int kda_gdr_bwd(const void* q, const void* k, const void* v, const void* g, cons
     rc = device_setup(&dev, &P.fwd.err, &sms);
     if (rc != KDA_OK) return rc;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const BwdLayout L = bwd_layout(varlen, B, T, Hk, Hv, N);
+    const BwdLayout L = bwd_layout(varlen, B, T, Hv, N);
     unsigned char* scratch = nullptr;
     cudaError_t e = cudaMallocAsync(reinterpret_cast<void**>(&scratch), L.total, s);
     if (e != cudaSuccess) return cuda_fail(KDA_ERR_ALLOC, e);
@@ -489,7 +488,6 @@ int kda_gdr_bwd(const void* q, const void* k, const void* v, const void* g, cons
     P.in.dout = static_cast<const __nv_bfloat16*>(d_out);
     P.in.dfinal = d_final_state;
     P.in.dfinal_dtype = d_final_state_dtype;
-    P.in.amax = reinterpret_cast<unsigned*>(scratch + L.amax);
     P.dstates = scratch + L.dstates;
     P.ys = scratch + L.ys;
     P.dq = static_cast<__nv_bfloat16*>(dq);
@@ -507,7 +505,6 @@ int kda_gdr_bwd(const void* q, const void* k, const void* v, const void* g, cons
         e = timed_launch(KDA_KERNEL_GDR_MAP, s,
                          [&] { return launch_gdr_map(in, first, first + N + 2, first + N + 1, P.fwd.err, s); });
     }
-    if (e == cudaSuccess) e = cudaMemsetAsync(P.in.amax, 0, (size_t)N * Hk * 4, s);
     if (e == cudaSuccess) e = timed_launch(KDA_KERNEL_GDR_PREP, s, [&] { return launch_gdr_prep(P, sms, s); });
     if (e == cudaSuccess)
         e = run_backward(P, chunks_first(P, sms, s), reinterpret_cast<float*>(scratch + L.carry), sms, s);

@@ -20,10 +20,11 @@
 //   dG of the last token also gets sum k.dK's first term + e^GC <S, dS>
 //   dg = suffix sums of dG inside the chunk.
 //
-// Operands are fp16, with the incoming gradients scaled by a power of two per (sequence,
-// key head) (grad_scale) and scale folded into dO; sums and states are fp32.  Gradients of
-// queries and keys that a group of value heads shares are summed in registers by one CTA, in a
-// fixed order.
+// Operands are fp16: S and X times 2^scale of the forward chain, dO (with `scale` folded in), dS and Y times 2^scale of the
+// backward one (kda_gdr_chunk.cuh), a chunk and value head's sums times the product of both; sums are fp32.  dP and dB
+// are products of two such operands, and are rounded to fp16 times a power of two of each 16 x 16 block's own where their size asks
+// for one.  Gradients of queries and keys that a group of value heads shares are summed in registers by one CTA, in a
+// fixed order, times the smallest 2^scale of the group's so far.
 #include <algorithm>
 
 #include "kda_gdr_chunk.cuh"
@@ -63,7 +64,9 @@ struct ChunkSmem {
     float col[4][kC];         // column sums of dP . Q K^T + dB . K K^T, one slot per 16 rows
     float yv[kParts][kC];
     float dot[kChunkThreads / 32];
+    int block[kChunkThreads / 32];   // exponents that blocks of dP and dB are held with, kEmpty without one
 };
+constexpr int kEmpty = 1000;
 
 // ldmatrix addresses in a tile kept in units: 16 rows from r0, units u0 and u0 + 1, in the
 // orders of a_addr and b_addr
@@ -143,6 +146,15 @@ __device__ __forceinline__ float4 peer_float4(const float* p, int rank) {
     return x;
 }
 
+// an operand's fragment times `by` (a power of two)
+__device__ __forceinline__ void times(uint32_t (&f)[4], __half2 by) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __half2 x = __hmul2(*reinterpret_cast<const __half2*>(&f[i]), by);
+        f[i] = *reinterpret_cast<const uint32_t*>(&x);
+    }
+}
+
 __device__ __forceinline__ void store_gate(void* p, int dtype, size_t i, float x) {
     if (dtype == KDA_F32) static_cast<float*>(p)[i] = x;
     else static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(x);
@@ -212,13 +224,24 @@ __global__ void __launch_bounds__(kChunkThreads, 1) gdr_bwd_chunk_kernel(GdrBack
         const int blocks = (rows + 15) / 16;
         const bool mine = rw < blocks;
         const long long tok = now.tok;
-        const float sigma = grad_scale(B.in.amax[(size_t)now.n * I.Hk + hk]), back = 1.0f / sigma;
         const uint32_t sk = smem_u32(S.k[kq]), sq = smem_u32(S.q[kq]);
 #pragma unroll
         for (int j = 0; j < 4; ++j)
 #pragma unroll
             for (int e = 0; e < 4; ++e) dq[j][e] = dk[j][e] = 0.0f;
         const int h0 = hk * share + rank, step = kSplit ? split : 1;
+        int unit = 0;                          // dq and dk are held times 2^unit
+        const auto lower_unit = [&](int to) {
+            const float by = power_of_two(to - unit);
+            unit = to;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    dq[j][e] *= by;
+                    dk[j][e] *= by;
+                }
+        };
         for (int h = h0; h < (hk + 1) * share; h += step, turn ^= 1) {
             const bool last = h + step >= (hk + 1) * share;
             const Place& then = last ? next : now;             // where the head after this one is
@@ -234,8 +257,15 @@ __global__ void __launch_bounds__(kChunkThreads, 1) gdr_bwd_chunk_kernel(GdrBack
 #pragma unroll
                 for (int m = 0; m < 4; ++m)
                     v[i][m] = (m & 1 ? i1 : i0) < rows ? __ldg(reinterpret_cast<const uint32_t*>(vp + (m & 1 ? 8 * I.v_stride : 0) + 16 * i + 8 * (m >> 1))) : 0u;
+            // the exponents of S and X, and of dO, dS and Y
+            const int* scales = reinterpret_cast<const int*>(P.blocks + ((size_t)now.chunk * I.Hv + h) * kBlockBytes + 2 * kTileBytes);
+            const int held = scales[kGateScale] + scales[kGateGradScale];
+            const float by = I.scale * power_of_two(scales[kGateGradScale]);
+            if (h == h0) unit = held;
+            else if (held < unit) lower_unit(held);
+            const float f = power_of_two(unit - held);
             asm volatile("cp.async.wait_all;\n" ::: "memory");
-            rows_to_half(S.o, I.scale * sigma, tid);
+            rows_to_half(S.o, by, tid);
             if (h == h0) {
                 rows_to_half(S.k[kq], 1.0f, tid);
                 rows_to_half(S.q[kq], 1.0f, tid);
@@ -283,6 +313,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) gdr_bwd_chunk_kernel(GdrBack
 #pragma unroll
                     for (int r = 0; r < 4; ++r) S.row[r][part][i0] = S.row[r][part][i1] = 0.0f;
                 if (lane < 16) S.col[rw][16 * part + lane] = 0.0f;
+                if (lane == 0) S.block[w] = kEmpty;
             }
             // <S, dS>: the diagonal of S^T dS, rows 16 (w / 2) .. over half of the key channels
             {
@@ -322,14 +353,14 @@ __global__ void __launch_bounds__(kChunkThreads, 1) gdr_bwd_chunk_kernel(GdrBack
                     }
                 }
                 // dP, dB and the sums of dP . Q K^T + dB . K K^T (M . Q K^T is P)
-                uint32_t fp[2][2], fb[2][2];
+                float pv[2][4], bv[2][4], top = 0.0f;
                 float rs0 = 0.0f, rs1 = 0.0f, bs0 = 0.0f, bs1 = 0.0f;
                 {
                     const float g0 = gate[kGateG + i0], g1 = gate[kGateG + i1];
 #pragma unroll
                     for (int nt = 0; nt < 2; ++nt) {
                         const int j = 16 * part + 8 * nt + 2 * t;
-                        float cs[2] = {0.0f, 0.0f}, pv[4], bv[4];
+                        float cs[2] = {0.0f, 0.0f};
                         const float2 gj = *reinterpret_cast<const float2*>(gate + kGateG + j);
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
@@ -339,17 +370,14 @@ __global__ void __launch_bounds__(kChunkThreads, 1) gdr_bwd_chunk_kernel(GdrBack
                                 pg + i * 128 + (((jj >> 3) ^ (i & 7)) << 4) + (jj & 7) * 2));
                             const float mk = jj < i ? m * kk[nt][e] : 0.0f;
                             const float dpv = dp[nt][e], dav = -da[nt][e], bi = e < 2 ? b0 : b1;
-                            pv[e] = jj <= i ? m * dpv : 0.0f;
-                            bv[e] = jj < i ? bi * m * dav : 0.0f;
+                            pv[nt][e] = jj <= i ? m * dpv : 0.0f;
+                            bv[nt][e] = jj < i ? bi * m * dav : 0.0f;
+                            top = fmaxf(top, fmaxf(fabsf(pv[nt][e]), fabsf(bv[nt][e])));
                             const float sum = (jj <= i ? dpv * pq : 0.0f) + bi * dav * mk;
                             cs[e & 1] += sum;
                             (e < 2 ? rs0 : rs1) += sum;
                             (e < 2 ? bs0 : bs1) += dav * mk;
                         }
-                        fp[nt][0] = pack_half2(pv[0], pv[1]);
-                        fp[nt][1] = pack_half2(pv[2], pv[3]);
-                        fb[nt][0] = pack_half2(bv[0], bv[1]);
-                        fb[nt][1] = pack_half2(bv[2], bv[3]);
                         cs[0] = rows_sum(cs[0]);
                         cs[1] = rows_sum(cs[1]);
                         if (g == 0) {
@@ -363,8 +391,21 @@ __global__ void __launch_bounds__(kChunkThreads, 1) gdr_bwd_chunk_kernel(GdrBack
                         S.row[4][part][i0] = bs0; S.row[4][part][i1] = bs1;
                     }
                 }
-                stsm(a_addr<128>(sdp, 16 * rw, 2 * part, lane), fp[0][0], fp[0][1], fp[1][0], fp[1][1]);
-                stsm(a_addr<128>(sdb, 16 * rw, 2 * part, lane), fb[0][0], fb[0][1], fb[1][0], fb[1][1]);
+                const int e = exponent_of(__uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(top))));
+                const int own = next_scale(0, e, -8, 14, 8);
+                if (lane == 0) S.block[w] = e == kNothing ? kEmpty : own;
+                if (own) {
+                    const float up = power_of_two(own);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        pv[j >> 2][j & 3] *= up;
+                        bv[j >> 2][j & 3] *= up;
+                    }
+                }
+                stsm(a_addr<128>(sdp, 16 * rw, 2 * part, lane), pack_half2(pv[0][0], pv[0][1]), pack_half2(pv[0][2], pv[0][3]),
+                     pack_half2(pv[1][0], pv[1][1]), pack_half2(pv[1][2], pv[1][3]));
+                stsm(a_addr<128>(sdb, 16 * rw, 2 * part, lane), pack_half2(bv[0][0], bv[0][1]), pack_half2(bv[0][2], bv[0][3]),
+                     pack_half2(bv[1][0], bv[1][1]), pack_half2(bv[1][2], bv[1][3]));
             }
             // dO S^T and Y S^T: this warp's rows, 32 key channels, over 128 value channels
             if (mine) {
@@ -388,6 +429,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) gdr_bwd_chunk_kernel(GdrBack
                         mma_f16(z[2 * np + 1], fy, b[2], b[3]);
                     }
                 }
+                const float fb0 = f * be0, fb1 = f * be1;
                 float qa0 = 0.0f, qa1 = 0.0f, kz0 = 0.0f, kz1 = 0.0f;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
@@ -399,9 +441,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1) gdr_bwd_chunk_kernel(GdrBack
                     qa1 += q1.x * a[j][2] + q1.y * a[j][3];
                     kz0 += k0.x * z[j][0] + k0.y * z[j][1];
                     kz1 += k1.x * z[j][2] + k1.y * z[j][3];
-                    dq[j][0] += a[j][0]; dq[j][1] += a[j][1]; dq[j][2] += a[j][2]; dq[j][3] += a[j][3];
-                    dk[j][0] -= be0 * z[j][0]; dk[j][1] -= be0 * z[j][1];
-                    dk[j][2] -= be1 * z[j][2]; dk[j][3] -= be1 * z[j][3];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        dq[j][e] = fmaf(f, a[j][e], dq[j][e]);
+                        dk[j][e] = fmaf(-(e < 2 ? fb0 : fb1), z[j][e], dk[j][e]);
+                    }
                 }
                 qa0 = quad_sum(qa0); qa1 = quad_sum(qa1); kz0 = quad_sum(kz0); kz1 = quad_sum(kz1);
                 if (t == 0) {
@@ -437,7 +481,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) gdr_bwd_chunk_kernel(GdrBack
                     a[j][0] *= f0; a[j][1] *= f0; a[j][2] *= f1; a[j][3] *= f1;
                     ka0 += k0.x * a[j][0] + k0.y * a[j][1];
                     ka1 += k1.x * a[j][2] + k1.y * a[j][3];
-                    dk[j][0] += a[j][0]; dk[j][1] += a[j][1]; dk[j][2] += a[j][2]; dk[j][3] += a[j][3];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) dk[j][e] = fmaf(f, a[j][e], dk[j][e]);
                 }
                 ka0 = quad_sum(ka0); ka1 = quad_sum(ka1);
                 if (t == 0) {
@@ -446,7 +491,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1) gdr_bwd_chunk_kernel(GdrBack
             }
             __syncthreads();               // dS and X have been read, all sums are there
             if (follows) fetch_second(then, then_h);
-            // dQ += dP K, dK += dP^T Q + dB K + dB^T K
+            // dQ += dP K, dK += dP^T Q + dB K + dB^T K, with all blocks brought to the sums' exponent
+            const int block = lane < kChunkThreads / 32 ? S.block[lane] : kEmpty;
+            const int least = __reduce_min_sync(0xFFFFFFFFu, block);
+            if (least != kEmpty && held + least < unit) lower_unit(held + least);
+            const int move = block == kEmpty ? 0 : max(unit - held - block, -40);      // at most 0
+            const bool moves = __any_sync(0xFFFFFFFFu, move != 0);
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks) {
                 if (!mine || ks >= blocks) break;
@@ -458,6 +508,18 @@ __global__ void __launch_bounds__(kChunkThreads, 1) gdr_bwd_chunk_kernel(GdrBack
                 if (ks >= rw) {            // transposed: from their own on
                     ldsm_t(fpt, b_addr<128>(sdp, 16 * ks, 2 * rw, lane));
                     ldsm_t(fbt, b_addr<128>(sdb, 16 * ks, 2 * rw, lane));
+                }
+                if (moves) {
+                    const __half2 n = __float2half2_rn(power_of_two(__shfl_sync(0xFFFFFFFFu, move, rw + 4 * ks)));
+                    const __half2 r = __float2half2_rn(power_of_two(__shfl_sync(0xFFFFFFFFu, move, ks + 4 * rw)));
+                    if (ks <= rw) {
+                        times(fpn, n);
+                        times(fbn, n);
+                    }
+                    if (ks >= rw) {
+                        times(fpt, r);
+                        times(fbt, r);
+                    }
                 }
 #pragma unroll
                 for (int np = 0; np < 2; ++np) {
@@ -480,6 +542,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) gdr_bwd_chunk_kernel(GdrBack
             }
             // gates: two tokens per lane of one warp
             if (w == 0) {
+                const int es = reinterpret_cast<const int*>(gate)[kGateScale], eg = reinterpret_cast<const int*>(gate)[kGateGradScale];
                 float dgv[2], ka[2];
 #pragma unroll
                 for (int m = 0; m < 2; ++m) {
@@ -491,7 +554,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) gdr_bwd_chunk_kernel(GdrBack
                     dgv[m] = qa - ka[m] - gate[kGateBe + j] * kz + rs - cs;
                     if (j < rows)
                         store_gate(B.dbeta, I.gate_dtype, (size_t)(tok + j) * I.Hv + h,
-                                   back * (yv - gate[kGateE + j] * kz + bs));
+                                   power_of_two(-eg) * (yv + power_of_two(-es) * (bs - gate[kGateE + j] * kz)));
                 }
                 float all = ka[0] + ka[1];
 #pragma unroll
@@ -506,11 +569,18 @@ __global__ void __launch_bounds__(kChunkThreads, 1) gdr_bwd_chunk_kernel(GdrBack
                     const float y = __shfl_down_sync(0xFFFFFFFFu, x, o);
                     if (lane + o < 32) x += y;
                 }
-                if (2 * lane < rows) store_gate(B.dg, I.gate_dtype, (size_t)(tok + 2 * lane) * I.Hv + h, back * x);
+                if (2 * lane < rows) store_gate(B.dg, I.gate_dtype, (size_t)(tok + 2 * lane) * I.Hv + h, times_power(x, -held));
                 if (2 * lane + 1 < rows)
-                    store_gate(B.dg, I.gate_dtype, (size_t)(tok + 2 * lane + 1) * I.Hv + h, back * (x - dgv[0]));
+                    store_gate(B.dg, I.gate_dtype, (size_t)(tok + 2 * lane + 1) * I.Hv + h, times_power(x - dgv[0], -held));
             }
         }
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                dq[j][e] = times_power(dq[j][e], -unit);
+                dk[j][e] = times_power(dk[j][e], -unit);
+            }
         if constexpr (kSplit) {            // in place of S and dS: fp32 rows, 8-channel groups turned by the row
             float* mine[2] = {reinterpret_cast<float*>(S.s), reinterpret_cast<float*>(S.ds)};
 #pragma unroll
@@ -534,7 +604,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) gdr_bwd_chunk_kernel(GdrBack
                 }
                 if (row < rows)
                     *reinterpret_cast<uint2*>((side ? B.dk : B.dq) + ((size_t)(tok + row) * I.Hk + hk) * kDim + ch) =
-                        make_uint2(pack_bf16(back * sum.x, back * sum.y), pack_bf16(back * sum.z, back * sum.w));
+                        make_uint2(pack_bf16(sum.x, sum.y), pack_bf16(sum.z, sum.w));
             }
             cluster_arrive();                  // until then the others read this CTA's part
             cluster_wait();
@@ -544,13 +614,13 @@ __global__ void __launch_bounds__(kChunkThreads, 1) gdr_bwd_chunk_kernel(GdrBack
                 const int ch = 32 * part + 8 * j + 2 * t;
                 if (i0 < rows) {
                     const size_t o = ((size_t)(tok + i0) * I.Hk + hk) * kDim + ch;
-                    *reinterpret_cast<uint32_t*>(B.dq + o) = pack_bf16(back * dq[j][0], back * dq[j][1]);
-                    *reinterpret_cast<uint32_t*>(B.dk + o) = pack_bf16(back * dk[j][0], back * dk[j][1]);
+                    *reinterpret_cast<uint32_t*>(B.dq + o) = pack_bf16(dq[j][0], dq[j][1]);
+                    *reinterpret_cast<uint32_t*>(B.dk + o) = pack_bf16(dk[j][0], dk[j][1]);
                 }
                 if (i1 < rows) {
                     const size_t o = ((size_t)(tok + i1) * I.Hk + hk) * kDim + ch;
-                    *reinterpret_cast<uint32_t*>(B.dq + o) = pack_bf16(back * dq[j][2], back * dq[j][3]);
-                    *reinterpret_cast<uint32_t*>(B.dk + o) = pack_bf16(back * dk[j][2], back * dk[j][3]);
+                    *reinterpret_cast<uint32_t*>(B.dq + o) = pack_bf16(dq[j][2], dq[j][3]);
+                    *reinterpret_cast<uint32_t*>(B.dk + o) = pack_bf16(dk[j][2], dk[j][3]);
                 }
             }
         }

@@ -3,13 +3,15 @@
 //
 // The mirror image of the forward chain (kda_gdr_chain.cuh), with the same roles and the same
 // hand-over between them; the gradient dS^T of the state (lane = value channel) is an fp32
-// accumulator in tensor memory, times grad_scale throughout, and
+// accumulator in tensor memory, and
 //
 //   dX^T = dO^T P + DS16 (e^(GC-G) K)^T        N = 64     DS16 = fp16(dS^T)
 //   Y^T  = DX16 T                              N = 64     DX16 = fp16(dX^T)
 //   dS^T = e^GC dS^T + dO^T (e^G Q) + Y16 (-beta e^G K)   N = 128
 //
-// with dO = fp16(scale grad_scale dO).  Products with dO as the left operand read it from shared
+// with dO = fp16(scale dO), all of it times 2^scale (kda_gdr_chunk.cuh).  The warps that bring in dO are up to two
+// chunks ahead of the chain, so chunk i's scale (counted as the chain walks) comes from e^GC dS as chunk i - 2 began and
+// dO of the three, with the decay in between.  Products with dO as the left operand read it from shared
 // memory (channels contiguous: MN-major) and are off the chain.  The state warps also write
 // DS16 and Y16 of every chunk to memory; four warps write dV = beta Y.
 //
@@ -26,9 +28,10 @@ constexpr int kStages = 2;
 constexpr int kOutWarps = 4;
 constexpr int kFirstKeys = kStateWarps + kOutWarps, kFirstQueries = kFirstKeys + kProducers / 32,
               kMmaWarp = kFirstQueries + kProducers / 32;
+constexpr int kScaleWarp = kMmaWarp + 1;
 constexpr int kBackThreads = 32 * (kMmaWarp + 4);
-// registers of a thread: 80 at launch, then by role (2 x 104 + 72 + 72 + 96 + 32 = 6 x 80)
-constexpr int kStateRegs = 104, kOutRegs = 72, kKeyRegs = 72, kQueryRegs = 96, kMmaRegs = 32;
+// registers of a thread: 80 at launch, then by role (2 x 112 + 64 + 72 + 88 + 32 = 6 x 80)
+constexpr int kStateRegs = 112, kOutRegs = 64, kKeyRegs = 72, kQueryRegs = 88, kMmaRegs = 32;
 // tensor memory columns; the accumulators of dX and Y alternate between two buffers
 constexpr uint32_t kTmS = 0, kTmS16 = 128, kTmX16 = 192, kTmY16 = 224, kTmAcc = 256, kTmCols = 512;
 
@@ -45,8 +48,11 @@ struct BackSmem {
     uint64_t s16, x16, y16;                   // operands written by the state warps
     uint64_t acc, y, s_done;                  // products done
     uint64_t y_free, done, drain;
+    uint64_t begun, ready;                    // the last state's gradient's exponents, the first two scales are there
+    ScaleRing scales;                         // published: of that gradient, then of e^GC dS of the chunk before
     uint32_t tmem;
 };
+
 static_assert(sizeof(BackSmem::Stage) % 1024 == 0, "the 128-byte swizzle wants 1,024-byte alignment");
 
 // ---- producers ----------------------------------------------------------------------------
@@ -74,6 +80,7 @@ __device__ void back_keys(const GdrBackward& B, BackSmem& S, const Span& span, i
     float ga = gate[(nch - 1) * (step / 4)];
     ahead(nch - 2);
     ahead(nch - 3);
+#pragma unroll 1
     for (int i = 0; i < nch; ++i) {
         const int c = nch - 1 - i, st = i % kStages;
         const unsigned phase = (unsigned)((i / kStages) & 1);
@@ -104,7 +111,7 @@ __device__ void back_keys(const GdrBackward& B, BackSmem& S, const Span& span, i
 }
 
 // one for queries and the outputs' gradients
-__device__ void back_queries(const GdrBackward& B, BackSmem& S, const Span& span, int nch, int h, float by, int p) {
+__device__ void back_queries(const GdrBackward& B, BackSmem& S, const Span& span, int nch, int h, int p) {
     const GdrChunked& P = B.fwd;
     const GdrInputs& I = P.in;
     const int hk = h / (I.Hv / I.Hk), unit = p & 15, row0 = p >> 4, lane = p & 31;
@@ -123,10 +130,13 @@ __device__ void back_queries(const GdrBackward& B, BackSmem& S, const Span& span
     float ga = gate[(nch - 1) * step];
     ahead(nch - 2);
     ahead(nch - 3);
+    if (!bar_wait(&S.ready, 0u, P.err)) return;
+#pragma unroll 1
     for (int i = 0; i < nch; ++i) {
         const int c = nch - 1 - i, st = i % kStages;
         auto& G = S.stage[st];
         if (i >= kStages && !bar_wait(&S.empty[st], (unsigned)(((i / kStages) & 1) ^ 1), P.err)) return;
+        const float by = S.scales.in[i & 3];
 #pragma unroll
         for (int j = 0; j < kTokenRows; ++j) {
             *reinterpret_cast<uint4*>(G.q + dst + 1024 * j) = scaled_half8(q.x[j], __shfl_sync(0xFFFFFFFFu, ga, (lane & 16) + j));
@@ -167,6 +177,7 @@ __device__ void back_issue(const GdrBackward& B, BackSmem& S, int nch, uint32_t 
     };
     if (!there(0)) return;
     begin(0);
+#pragma unroll 1
     for (int i = 0; i < nch; ++i) {
         const unsigned turn = (unsigned)(i & 1);
         const uint32_t stage = stage_of(i), acc = tmem + kTmAcc + 64 * uniform(turn), on = tc::elect();
@@ -177,19 +188,22 @@ __device__ void back_issue(const GdrBackward& B, BackSmem& S, int nch, uint32_t 
         if (!wait(S.x16, turn)) return;
         product_mn(acc, tmem + kTmX16, stage + offsetof(BackSmem::Stage, t), kId64, false, on);
         tc::commit_on(smem_u32(&S.y), on);
+        tc::arrive_on(smem_u32(&S.y), on);   // hands on the scales, too
         from_o(tmem + kTmS, stage, offsetof(BackSmem::Stage, q), kId128, true);
         if (i + 1 < nch && !there(i + 1)) return;
         if (!wait(S.y16, turn)) return;
         product_mn(tmem + kTmS, tmem + kTmY16, stage + offsetof(BackSmem::Stage, kb), kId128, true, on);
         tc::commit_on(smem_u32(&S.s_done), on);
+        tc::arrive_on(smem_u32(&S.s_done), on);
         tc::commit_on(smem_u32(&S.empty[i % kStages]), on);
+        tc::arrive_on(smem_u32(&S.empty[i % kStages]), on);
         if (i + 1 < nch) begin(i + 1);
     }
 }
 
 // ---- state warps ----------------------------------------------------------------------------
 __device__ void back_states(const GdrBackward& B, BackSmem& S, const Span& span, int nch, int w, int lane, size_t sbase,
-                            int h, float sigma, uint32_t tmem) {
+                            int h, uint32_t tmem) {
     const GdrChunked& P = B.fwd;
     const int half = w >> 2, v = 32 * (w & 3) + lane;
     const uint32_t tl = tmem + ((uint32_t)(32 * (w & 3)) << 16);
@@ -199,9 +213,17 @@ __device__ void back_states(const GdrBackward& B, BackSmem& S, const Span& span,
     const size_t d_step = (size_t)P.in.Hv * (kBlockBytes / 4);
     float d = nch > 0 ? dp[(nch - 1) * d_step] : 0.0f;
     uint32_t x[2][32];
-#pragma unroll
-    for (int i = 0; i < 64; ++i)
-        x[i >> 5][i & 31] = __float_as_uint(B.in.dfinal ? sigma * load_state(B.in.dfinal, B.in.dfinal_dtype, at + (size_t)i * kDim) : 0.0f);
+    load_state(x, B.in.dfinal, B.in.dfinal_dtype, at);
+    if (nch > 0) {
+        if (B.in.dfinal) {
+            publish(S.scales.top[0][w], x, lane);
+            if (lane == 0) bar_arrive(&S.begun);
+        }
+        if (!bar_wait(&S.ready, 0u, P.err)) return;
+        scale32(x[0], S.scales.ratio[0]);
+        scale32(x[1], S.scales.ratio[0]);
+    }
+#pragma unroll 1
     for (int i = 0; i < nch; ++i) {
         const int c = nch - 1 - i;
         const unsigned turn = (unsigned)(i & 1);
@@ -218,6 +240,7 @@ __device__ void back_states(const GdrBackward& B, BackSmem& S, const Span& span,
         const size_t unit = (size_t)(span.chunk + c) * P.in.Hv + h;
         keep_units(B.dstates + unit * kStateTile, v, 8 * half, f[0]);
         keep_units(B.dstates + unit * kStateTile, v, 8 * half + 4, f[1]);
+        publish(S.scales.top[(i + 1) & 3][w], f, d, lane);
         uint32_t y[32];
         if (!bar_wait(&S.acc, turn, P.err)) return;
         tc::fence_after_sync();
@@ -237,32 +260,81 @@ __device__ void back_states(const GdrBackward& B, BackSmem& S, const Span& span,
         d = next_d;
         if (!bar_wait(&S.s_done, turn, P.err)) return;
         tc::fence_after_sync();
+        const float ratio = S.scales.ratio[(i + 1) & 3];
+        if (__builtin_expect(c > 0 && ratio != 1.0f, 0)) rescale(tl + kTmS + 64 * half, ratio);
         tc::ld32(tl + kTmS + 64 * half, x[0]);
         tc::ld32(tl + kTmS + 64 * half + 32, x[1]);
         tc::wait_ld();
     }
-    if (B.dinit) {
-        const float back = 1.0f / sigma;
-#pragma unroll
-        for (int i = 0; i < 64; ++i)
-            store_state(B.dinit, B.dinit_dtype, at + (size_t)i * kDim, back * __uint_as_float(x[i >> 5][i & 31]));
+    if (B.dinit) store_state(x, nch > 0 ? S.scales.out[(nch - 1) & 3] : 1.0f, B.dinit, B.dinit_dtype, at);
+}
+
+// ---- scales (one warp) ------------------------------------------------------------------------
+// Chunk i + 2's once the state warps have published e^GC dS of chunk i (with dX16); Y16's barrier hands the choice
+// to the issuing warp and its arrivals to everyone else.
+__device__ void back_scales(const GdrBackward& B, BackSmem& S, const Span& span, int nch, int h, int lane) {
+    const GdrChunked& P = B.fwd;
+    const size_t step = (size_t)P.in.Hv * (kBlockBytes / 4);
+    float* gates = reinterpret_cast<float*>(P.blocks + ((size_t)(span.chunk + nch - 1) * P.in.Hv + h) * kBlockBytes + 2 * kTileBytes);
+    const auto d_o = [&](int i) { return i < nch ? *reinterpret_cast<const unsigned*>(gates - i * step + kGateDo) : 0u; };
+    const auto decay = [&](int i) { return i < nch ? gates[kGateAll - (ptrdiff_t)(i * step)] : 0.0f; };
+    int scale = 0, one = kNothing, two = kNothing;    // exponents of dO one and two chunks back
+    const auto next = [&](int i, int before, unsigned bytes) {
+        const int now = exponent_of_bytes(bytes), last = scale;
+        scale = gradient_scale(scale, max(before, max(one, now)));
+        two = one;
+        one = now;
+        if (lane != 0 || i >= nch) return;
+        S.scales.ratio[i & 3] = power_of_two(min(scale - last, 127));
+        S.scales.in[i & 3] = P.in.scale * power_of_two(scale);
+        S.scales.out[i & 3] = power_of_two(-scale);
+        reinterpret_cast<int*>(gates - i * step)[kGateGradScale] = scale;
+    };
+    const auto product = [](int a, int b) { return max(a + b, kNothing); };      // of exponents
+    unsigned ahead = d_o(2);
+    float fade = decay(1);
+    const unsigned first = d_o(0), second = d_o(1);
+    const int fade0 = exponent_of(decay(0));
+    if (B.in.dfinal && !bar_wait(&S.begun, 0u, P.err)) return;
+    const int begun = published(S.scales, 0, 0);
+    next(0, begun, first);
+    int held = scale;                         // chunk i's scale, in which e^GC dS is published
+    next(1, product(begun, fade0), second);
+    __syncwarp();
+    if (lane == 0) bar_arrive(&S.ready);
+#pragma unroll 1
+    for (int i = 0; i < nch; ++i) {
+        if (!bar_wait(&S.x16, (unsigned)(i & 1), P.err)) return;
+        if (i + 2 < nch) {
+            const int now = exponent_of(fade);
+            const unsigned bytes = ahead;
+            ahead = d_o(i + 3);
+            fade = decay(i + 2);
+            const int before = product(max(published(S.scales, i + 1, held), two), now);
+            held = scale;
+            next(i + 2, before, bytes);
+        }
+        __syncwarp();
+        if (lane == 0) bar_arrive(&S.y16);
     }
 }
 
 // ---- output warps: dV = beta Y ---------------------------------------------------------------
 __device__ void back_outputs(const GdrBackward& B, BackSmem& S, const Span& span, int nch, int w, int lane, int h,
-                             float back, uint32_t tmem) {
+                             uint32_t tmem) {
     const GdrChunked& P = B.fwd;
     const uint32_t tl = tmem + ((uint32_t)(32 * (w & 3)) << 16);
     const size_t step = (size_t)P.in.Hv * kDim;
+#pragma unroll 1
     for (int i = 0; i < nch; ++i) {
         const int c = nch - 1 - i;
         const unsigned turn = (unsigned)(i & 1);
-        // beta / sigma of tokens 2 lane and 2 lane + 1
+        // beta / 2^scale of tokens 2 lane and 2 lane + 1
         float2 b = reinterpret_cast<const float2*>(P.blocks + ((size_t)(span.chunk + c) * P.in.Hv + h) * kBlockBytes +
                                                    2 * kTileBytes + 4 * kGateB)[lane];
         if (!bar_wait(&S.y, turn, P.err)) return;
         tc::fence_after_sync();
+        const float back = S.scales.out[i & 3];
         b.x *= back;
         b.y *= back;
         store_tokens(B.dv + (span.start + (long long)c * kC) * step + h * kDim + 32 * (w & 3), step,
@@ -283,19 +355,21 @@ __device__ __forceinline__ void back_run(const GdrBackward& B, BackSmem& S, int 
     const Span span = span_of(I, P.chunks, n);
     const int nch = (int)uniform((span.len + kC - 1) / kC);
     const int tid = threadIdx.x, lane = tid & 31, w = (int)uniform(tid >> 5);
-    const float sigma = grad_scale(B.in.amax[(size_t)n * I.Hk + h / (I.Hv / I.Hk)]);
     if (tid == 0) {
         for (int i = 0; i < kStages; ++i) {
             bar_init(&S.full[i], 2 * kProducers);
             bar_init(&S.copied[i], 1);
-            bar_init(&S.empty[i], 1);
+            bar_init(&S.empty[i], 2);
         }
-        for (uint64_t* b : {&S.acc, &S.y, &S.s_done, &S.drain}) bar_init(b, 1);
-        for (uint64_t* b : {&S.s16, &S.x16, &S.y16}) bar_init(b, kStateWarps);
+        for (uint64_t* b : {&S.acc, &S.drain, &S.ready}) bar_init(b, 1);
+        for (uint64_t* b : {&S.y, &S.s_done}) bar_init(b, 2);
+        for (uint64_t* b : {&S.s16, &S.x16, &S.begun}) bar_init(b, kStateWarps);
+        bar_init(&S.y16, kStateWarps + 1);
         bar_init(&S.y_free, kOutWarps);
         bar_init(&S.done, kStateWarps + kOutWarps);
         asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     }
+    if (tid < kStateWarps) S.scales.top[0][tid] = kNothing;
     tc::fence_proxy_async_smem();
     if (w == kMmaWarp) {
         tc::tmem_alloc(smem_u32(&S.tmem), kTmCols);
@@ -308,21 +382,24 @@ __device__ __forceinline__ void back_run(const GdrBackward& B, BackSmem& S, int 
     const size_t sbase = ((size_t)n * I.Hv + h) * kDim * kDim;
     if (w < kStateWarps) {
         tc::registers_up<kStateRegs>();
-        back_states(B, S, span, nch, w, lane, sbase, h, sigma, tmem);
+        back_states(B, S, span, nch, w, lane, sbase, h, tmem);
     } else if (w < kFirstKeys) {
         tc::registers_down<kOutRegs>();
-        back_outputs(B, S, span, nch, w, lane, h, 1.0f / sigma, tmem);
+        back_outputs(B, S, span, nch, w, lane, h, tmem);
     } else if (w < kFirstQueries) {
         tc::registers_down<kKeyRegs>();
         if (nch > 0) back_keys(B, S, span, nch, h, tid - 32 * kFirstKeys);
         return;
     } else if (w < kMmaWarp) {
         tc::registers_up<kQueryRegs>();
-        if (nch > 0) back_queries(B, S, span, nch, h, I.scale * sigma, tid - 32 * kFirstQueries);
+        if (nch > 0) back_queries(B, S, span, nch, h, tid - 32 * kFirstQueries);
         return;
     } else {
         tc::registers_down<kMmaRegs>();
-        if (w > kMmaWarp) return;
+        if (w > kMmaWarp) {
+            if (w == kScaleWarp && nch > 0) back_scales(B, S, span, nch, h, lane);
+            return;
+        }
         if (nch > 0) back_issue(B, S, nch, tmem);
         // every MMA and every arrival of this warp is over, and all other warps have left tensor
         // memory, before it is freed

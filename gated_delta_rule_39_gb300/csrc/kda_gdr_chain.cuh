@@ -12,12 +12,15 @@
 //
 // The left operands are fp16 in tensor memory; decays and signs are folded into the keys and
 // queries on their way to shared memory, and V enters R as a product with the identity (bf16,
-// exact), so that between two products the state warps only round an accumulator.
+// exact), so that between two products the state warps only round an accumulator.  V, R, X and S stand for
+// 2^scale times themselves (kda_gdr_chunk.cuh): the identity's ones are 2^scale, the state is multiplied
+// when the scale changes, and the outputs are multiplied back.  Chunk c's scale comes from e^GC S as chunk c - 1
+// began, and the values of both, so that it is known before chunk c's first product.
 //
 // Warps: 8 state warps (lane quarter w % 4, half of the columns each) do that rounding; one
 // warp issues the MMAs, those that the chain does not need behind the state's update;
-// 4 warps bring in keys, values, T and P of the next chunks, 4 the queries, and 4 write the
-// outputs.  Every role's loop is kept small: with the MMAs issued from a state warp, the
+// 4 warps bring in keys, values, T and P of the next chunks, 4 the queries, 4 write the
+// outputs, one chooses the scales and two find out how large the values are.  Every role's loop is kept small: with the MMAs issued from a state warp, the
 // others' jumps over that code cost 200 cycles each (instruction cache misses).
 // Measured: 1.6 us per chunk of 64 tokens (8,192 tokens x 96 heads on 96 SMs: 204 us; the same
 // chain with mma.sync and a warp per 16 channels took 645).  Of some 3,000 cycles the tensor core runs
@@ -39,7 +42,8 @@ constexpr int kStages = 3;                    // chunks in shared memory
 constexpr int kOutWarps = 4;
 constexpr int kFirstKeys = kStateWarps + kOutWarps, kFirstQueries = kFirstKeys + kProducers / 32,
               kMmaWarp = kFirstQueries + kProducers / 32;
-constexpr int kChainThreads = 32 * (kMmaWarp + 4);   // whole warpgroups: three warps of the last are idle
+constexpr int kScaleWarp = kMmaWarp + 1;
+constexpr int kChainThreads = 32 * (kMmaWarp + 4);   // whole warpgroups
 // registers of a thread: 80 at launch, then by role (2 x 112 + 64 + 72 + 80 + 40 = 6 x 80)
 constexpr int kStateRegs = 112, kOutRegs = 64, kKeyRegs = 72, kMmaRegs = 40;
 // tensor memory columns; S16 and O alternate between two buffers
@@ -60,6 +64,10 @@ struct ChainSmem {
     uint64_t acc, x, s_done;                  // products done
     uint64_t q_full, o_done[2], o_free[2];
     uint64_t done, drain;
+    uint64_t begun, ready;                    // the initial state's exponents, chunk 0's scale are there
+    uint64_t sized[kStages];
+    float largest[kStages][2];                // |V| of the halves of a stage's values
+    ScaleRing scales;                         // published: of the initial state, then of e^GC S of the chunk before
     uint32_t tmem;
 };
 static_assert(sizeof(ChainSmem::Stage) % 1024 == 0, "the 128-byte swizzle wants 1,024-byte alignment");
@@ -91,6 +99,7 @@ __device__ inline void keys(const GdrChunked& P, const CUtensorMap& vmap, ChainS
     float ga = gate[0];
     ahead(1);
     ahead(2);
+#pragma unroll 1
     for (int c = 0; c < nch; ++c) {
         const int st = c % kStages, rows = min(kC, span.len - c * kC);
         auto& G = S.stage[st];
@@ -140,6 +149,7 @@ __device__ inline void queries(const GdrChunked& P, ChainSmem& S, const Span& sp
     float ga = gate[0];
     prefetch_rows(I.q, I.q_stride, span, hk * kDim, 1, p);
     prefetch_rows(I.q, I.q_stride, span, hk * kDim, 2, p);
+#pragma unroll 1
     for (int c = 0; c < nch; ++c) {
         if (c > 0 && !bar_wait(&S.o_done[(c - 1) & 1], (unsigned)(((c - 1) >> 1) & 1), P.err)) return;   // the last ones have been used
 #pragma unroll
@@ -169,7 +179,7 @@ __device__ void issue(const GdrChunked& P, ChainSmem& S, int nch, uint32_t tmem)
         const unsigned phase = (unsigned)((c / kStages) & 1);
         return wait(S.copied[c % kStages], phase) && wait(S.full[c % kStages], phase);
     };
-    // R^T's part that does not need the state: V^T I
+    // R^T's part that does not need the state: V^T I, the identity's ones being 2^scale
     const auto begin = [&](int c) {
         const uint32_t on = tc::elect();
         const uint64_t dv = desc_mn(stage_of(c) + offsetof(ChainSmem::Stage, v), kHalfTile), de = desc_k(smem_u32(S.eye));
@@ -177,8 +187,9 @@ __device__ void issue(const GdrChunked& P, ChainSmem& S, int nch, uint32_t tmem)
         for (int k = 0; k < 4; ++k)
             tc::mma_ss_on(tmem + kTmAcc, dv + kstep_mn(k), de + kstep_k(k, 0), kId64 | tc::kIdBf16 | tc::kIdMnA, k > 0, on);
     };
-    if (!there(0)) return;
+    if (!wait(S.ready, 0u) || !there(0)) return;
     begin(0);
+#pragma unroll 1
     for (int c = 0; c < nch; ++c) {
         const unsigned turn = (unsigned)(c & 1), phase = (unsigned)((c >> 1) & 1);
         const uint32_t stage = stage_of(c), s16 = tmem + kTmS16 + 64 * uniform(turn), on = tc::elect();
@@ -195,11 +206,13 @@ __device__ void issue(const GdrChunked& P, ChainSmem& S, int nch, uint32_t tmem)
         if (!wait(S.x16, turn)) return;
         product_mn(tmem + kTmS, tmem + kTmX16, stage + offsetof(ChainSmem::Stage, kd), kId128, true, on);
         tc::commit_on(smem_u32(&S.s_done), on);
+        tc::arrive_on(smem_u32(&S.s_done), on);  // hands on the next scale, too
         if (!kSave) {                         // outputs
             const uint32_t o = tmem + kTmO + 64 * uniform(turn);
             product_k<8>(o, s16, smem_u32(S.q), kId64, false, on);
             product_k<4>(o, tmem + kTmX16, stage + offsetof(ChainSmem::Stage, tp) + kTileBytes, kId64, true, on);
             tc::commit_on(smem_u32(&S.o_done[turn]), on);
+            tc::arrive_on(smem_u32(&S.o_done[turn]), on);    // hands on the scale, too
         }
         if (c + 1 < nch) begin(c + 1);
         tc::commit_on(smem_u32(&S.empty[c % kStages]), on);
@@ -218,9 +231,17 @@ __device__ void states(const GdrChunked& P, ChainSmem& S, const Span& span, int 
     const size_t d_step = (size_t)P.in.Hv * (kBlockBytes / 4);
     float d = nch > 0 ? *dp : 0.0f;
     uint32_t x[2][32];
-#pragma unroll
-    for (int i = 0; i < 64; ++i)
-        x[i >> 5][i & 31] = __float_as_uint(P.init_state ? load_state(P.init_state, P.init_dtype, at + (size_t)i * kDim) : 0.0f);
+    load_state(x, P.init_state, P.init_dtype, at);
+    if (nch > 0) {
+        if (P.init_state) {
+            publish(S.scales.top[0][w], x, lane);
+            if (lane == 0) bar_arrive(&S.begun);
+        }
+        if (!bar_wait(&S.ready, 0u, P.err)) return;
+        scale32(x[0], S.scales.ratio[0]);
+        scale32(x[1], S.scales.ratio[0]);
+    }
+#pragma unroll 1
     for (int c = 0; c < nch; ++c) {
         const unsigned turn = (unsigned)(c & 1);
         const float next_d = c + 1 < nch ? dp[(c + 1) * d_step] : 0.0f;
@@ -240,6 +261,7 @@ __device__ void states(const GdrChunked& P, ChainSmem& S, const Span& span, int 
             keep_units(P.states + unit * kStateTile, v, 8 * half, f[0]);
             keep_units(P.states + unit * kStateTile, v, 8 * half + 4, f[1]);
         }
+        publish(S.scales.top[(c + 1) & 3][w], f, d, lane);
         uint32_t y[32];
         if (!bar_wait(&S.acc, turn, P.err)) return;
         tc::fence_after_sync();
@@ -259,14 +281,88 @@ __device__ void states(const GdrChunked& P, ChainSmem& S, const Span& span, int 
         d = next_d;
         if (!bar_wait(&S.s_done, turn, P.err)) return;
         tc::fence_after_sync();
+        const float ratio = S.scales.ratio[(c + 1) & 3];
+        if (__builtin_expect(c + 1 < nch && ratio != 1.0f, 0)) rescale(tl + kTmS + 64 * half, ratio);
         tc::ld32(tl + kTmS + 64 * half, x[0]);
         tc::ld32(tl + kTmS + 64 * half + 32, x[1]);
         tc::wait_ld();
     }
-    if (P.final_state)
+    if (P.final_state) store_state(x, nch > 0 ? S.scales.out[(nch - 1) & 3] : 1.0f, P.final_state, P.final_dtype, at);
+}
+
+// ---- sizes of the values (two warps, half a tile each) -------------------------------------------
+// They run ahead of the scales, but a stage is not given back before the scale warp's arrival for its chunk, which
+// comes after theirs: so neither the values nor a stage's barrier change while someone still needs them.
+__device__ inline void sizes(const GdrChunked& P, ChainSmem& S, int nch, int half, int lane) {
+#pragma unroll 1
+    for (int c = 0; c < nch; ++c) {
+        const int st = c % kStages;
+        const unsigned char* tile = S.stage[st].v + half * kHalfTile + 16 * lane;
+        const unsigned phase = (unsigned)((c / kStages) & 1);
+        if (!bar_wait(&S.copied[st], phase, P.err) || !bar_wait(&S.full[st], phase, P.err)) return;
+        __nv_bfloat162 top[4] = {};
+#pragma unroll 4
+        for (int i = 0; i < kHalfTile; i += 16 * 32) {
+            const uint4 u = *reinterpret_cast<const uint4*>(tile + i);
+            const uint32_t x[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-        for (int i = 0; i < 64; ++i)
-            store_state(P.final_state, P.final_dtype, at + (size_t)i * kDim, __uint_as_float(x[i >> 5][i & 31]));
+            for (int j = 0; j < 4; ++j) top[j] = __hmax2(top[j], __habs2(*reinterpret_cast<const __nv_bfloat162*>(&x[j])));
+        }
+        const float2 m = __bfloat1622float2(__hmax2(__hmax2(top[0], top[1]), __hmax2(top[2], top[3])));
+        const unsigned all = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(fmaxf(m.x, m.y)));
+        if (lane == 0) {
+            S.largest[st][half] = __uint_as_float(all);
+            bar_arrive(&S.sized[st]);
+        }
+    }
+}
+
+// ---- scales (one warp) ------------------------------------------------------------------------
+// Chunk c + 1's while chunk c's X is formed: what the state warps publish is there with R16, and X16's
+// barrier hands the choice to the issuing warp, with the identity as the next chunk wants it.
+template <bool kSave>
+__device__ void scales(const GdrChunked& P, ChainSmem& S, const Span& span, int nch, int h, int lane) {
+    float* gates = reinterpret_cast<float*>(P.blocks + ((size_t)span.chunk * P.in.Hv + h) * kBlockBytes + 2 * kTileBytes);
+    const size_t step = (size_t)P.in.Hv * (kBlockBytes / 4);
+    // the exponent of a chunk's largest value; false: the wait gave up
+    const auto values = [&](int c, int& e) {
+        const int st = c % kStages;
+        if (!bar_wait(&S.sized[st], (unsigned)((c / kStages) & 1), P.err)) return false;
+        e = exponent_of(fmaxf(S.largest[st][0], S.largest[st][1]));
+        return true;
+    };
+    const auto set = [&](int c, int scale, int before) {
+        if (lane != 0) return;
+        S.scales.ratio[c & 3] = power_of_two(min(scale - before, 127));
+        S.scales.out[c & 3] = power_of_two(-scale);
+        if (kSave) reinterpret_cast<int*>(gates + c * step)[kGateScale] = scale;
+    };
+    const auto identity = [&](int scale) {    // ones of 2^scale at (i, i)
+        for (int row = lane; row < kC; row += 32)
+            *reinterpret_cast<uint16_t*>(S.eye + row * 128 + (((row >> 3) ^ (row & 7)) << 4) + (row & 7) * 2) = (uint16_t)((scale + 127) << 7);
+        tc::fence_proxy_async_smem();
+    };
+    int v, next_v = kNothing;
+    if (!values(0, v) || (P.init_state && !bar_wait(&S.begun, 0u, P.err))) return;
+    int scale = forward_scale(0, max(published(S.scales, 0, 0), v));
+    if (scale) identity(scale);
+    set(0, scale, 0);
+    __syncwarp();
+    if (lane == 0) bar_arrive(&S.ready);
+#pragma unroll 1
+    for (int c = 0; c < nch; ++c) {
+        if (c + 1 < nch && !values(c + 1, next_v)) return;
+        if (!bar_wait(&S.r16, (unsigned)(c & 1), P.err)) return;
+        if (c + 1 < nch) {
+            const int next = forward_scale(scale, max(published(S.scales, c + 1, scale), max(v, next_v)));
+            v = next_v;
+            if (next != scale) identity(next);        // R is there: the last product with the identity is over
+            set(c + 1, next, scale);
+            scale = next;
+        }
+        __syncwarp();
+        if (lane == 0) bar_arrive(&S.x16);
+    }
 }
 
 // ---- output warps -----------------------------------------------------------------------------
@@ -275,13 +371,15 @@ __device__ inline void outputs(const GdrChunked& P, ChainSmem& S, const Span& sp
     const GdrInputs& I = P.in;
     const uint32_t tl = tmem + ((uint32_t)(32 * (w & 3)) << 16);
     const size_t step = (size_t)I.Hv * kDim;
+#pragma unroll 1
     for (int c = 0; c < nch; ++c) {
         const int buf = c & 1;
         if (!bar_wait(&S.o_done[buf], (unsigned)((c >> 1) & 1), P.err)) return;
         tc::fence_after_sync();
+        const float by = I.scale * S.scales.out[c & 3];
         store_tokens(P.out + (span.start + (long long)c * kC) * step + h * kDim + 32 * (w & 3), step,
                      min(kC, span.len - c * kC), tl + kTmO + 64 * buf, S.turn[w & 3], lane,
-                     [&](int) { return make_float2(I.scale, I.scale); },
+                     [&](int) { return make_float2(by, by); },
                      [&] {
                          __syncwarp();
                          if (lane == 0) bar_arrive(&S.o_free[buf]);
@@ -302,14 +400,19 @@ __device__ __forceinline__ void run(const GdrChunked& P, const CUtensorMap& vmap
             bar_init(&S.full[i], kProducers);
             bar_init(&S.copied[i], 1);
             bar_init(&S.empty[i], 1);
+            bar_init(&S.sized[i], 2);
         }
-        for (uint64_t* b : {&S.acc, &S.x, &S.s_done, &S.o_done[0], &S.o_done[1], &S.drain}) bar_init(b, 1);
-        for (uint64_t* b : {&S.s16, &S.r16, &S.x16}) bar_init(b, kStateWarps);
+        for (uint64_t* b : {&S.acc, &S.x, &S.drain, &S.ready}) bar_init(b, 1);
+        bar_init(&S.s_done, 2);
+        for (uint64_t* b : {&S.s16, &S.r16, &S.begun}) bar_init(b, kStateWarps);
+        bar_init(&S.x16, kStateWarps + 1);
+        for (int i = 0; i < 2; ++i) bar_init(&S.o_done[i], 2);
         bar_init(&S.q_full, kProducers / 32);
         for (int i = 0; i < 2; ++i) bar_init(&S.o_free[i], kOutWarps);
         bar_init(&S.done, kStateWarps + kOutWarps);
         asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     }
+    if (tid < kStateWarps) S.scales.top[0][tid] = kNothing;
     // the identity: 1 at (i, i)
     for (int i = tid; i < kTileBytes / 16; i += kChainThreads) {
         const int row = i >> 3, at = row & 7, hit = (i & 7) == (row >> 3);
@@ -343,7 +446,14 @@ __device__ __forceinline__ void run(const GdrChunked& P, const CUtensorMap& vmap
         return;
     } else {
         tc::registers_down<kMmaRegs>();
-        if (w > kMmaWarp) return;
+        if (w > kMmaWarp) {
+            if (w == kScaleWarp) {
+                if (nch > 0) scales<kSave>(P, S, span, nch, h, lane);
+            } else {
+                sizes(P, S, nch, w - kScaleWarp - 1, lane);
+            }
+            return;
+        }
         if (nch > 0) issue<kSave>(P, S, nch, tmem);
         // every MMA and every arrival of this warp is over, and all other warps have left tensor
         // memory, before it is freed

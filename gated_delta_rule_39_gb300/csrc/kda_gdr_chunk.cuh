@@ -16,8 +16,9 @@
 // between chunks.  The operands of the tensor-core products are fp16: queries, keys (bf16
 // data) times their decays, T beta, P, R, X and the rounded state.
 // fp16's 11 bits keep the result within 5e-4 of the exact one on unit keys, where bf16
-// operands gave 3e-3; its price is that keys, queries, values and states have to stay
-// below 65,504.  The inverse T is formed in fp32 with tf32 products between its blocks.
+// operands gave 3e-3.  Its price is its range: values, states and gradients are scaled for it (below);
+// queries, keys, q.k and the entries of T beta are not.  The inverse T is formed in fp32 with tf32 products
+// between its blocks.
 #pragma once
 #include "kda_cluster.cuh"
 #include "kda_gdr.cuh"
@@ -32,10 +33,12 @@ namespace gdr {
 constexpr int kC = 64;                        // tokens per chunk
 // One (chunk, value head)'s block of scratch: T beta (columns scaled) and P as fp16 [64][64]
 // tiles (128-byte rows whose 16-byte units are stored at unit ^ (row & 7)), then fp32 b, b e^G, e^G, e^(G_C - G)
-// and G (in base 2) of its 64 tokens, and e^(G_C).
+// and G (in base 2) of its 64 tokens, and of the whole chunk e^(G_C), the biased exponent of the largest
+// |scale dO| (of four parts of the rows, a byte each) and the scales (int) that the forward and the backward chain chose.
 constexpr int kTileBytes = kC * kC * 2;
 constexpr int kGateB = 0, kGateBe = kC, kGateE = 2 * kC, kGateEnd = 3 * kC, kGateG = 4 * kC, kGateAll = 5 * kC;
-constexpr int kGateFloats = 5 * kC + 4;
+constexpr int kGateDo = kGateAll + 1, kGateScale = kGateAll + 2, kGateGradScale = kGateAll + 3;
+constexpr int kGateFloats = kGateAll + 4;
 constexpr int kBlockUsed = 2 * kTileBytes + kGateFloats * 4;   // 17,680
 constexpr int kBlockBytes = (kBlockUsed + 127) / 128 * 128;
 
@@ -170,15 +173,36 @@ __device__ __forceinline__ int row_unit(int v, int u) { return (128 * u + v) * 1
 constexpr int kStateTile = kDim * kDim * 2;
 constexpr int kTokenTile = kDim * kC * 2;
 
-// Backward: the gradients that enter (scale dO, and that of the last state) are scaled, per
-// (sequence, key head), by the power of two that brings the largest to 16 .. 32, so that fp16 operands keep their precision
-// whatever the loss is scaled by.  `amax` holds the bits of the largest magnitude.
-__device__ __forceinline__ float grad_scale(unsigned amax) {
-    const int e = (int)(amax >> 23);                // biased exponent of the largest
-    if (e == 0 || e == 255) return 1.0f;            // zero (or subnormal); not finite
-    const int x = 127 + 4 - (e - 127);              // 2^(4 - exponent)
-    return __uint_as_float((unsigned)(x < 1 ? 1 : x > 253 ? 253 : x) << 23);
+// ---- scales -------------------------------------------------------------------------------
+// fp16 keeps its 11 bits between 2^-14 and 65,504.  All that a chain rounds to it is linear in V and
+// the initial state (S, R, X), or in the gradients that come in (dO, dS, dX, Y).  So a chain works on
+// them times a power of two, 2^scale, that it chooses again for every chunk from the exponent of
+// the largest of what enters there, and results of any size keep their accuracy.  A scale stays while that
+// exponent is in a window: forwards 2^-6 .. 2^6, so that ordinary values are taken as they are, and
+// backwards 2^-1 .. 2^7, where rows of dX and Y may be far apart.  Above it 9 bits are left for what a chunk's 64 tokens
+// and the two chunks that the choice does not know yet can add up to with queries and keys of length 1.
+constexpr int kNothing = -1000;            // exponent of zero and of what is not finite
+__device__ __forceinline__ int exponent_of(float x) {      // of a magnitude
+    const int e = (int)(__float_as_uint(x) >> 23);
+    return e == 0 || e == 255 ? kNothing : e - 127;
 }
+__device__ __forceinline__ int exponent_of_bytes(unsigned x) {       // the largest of four biased ones
+    x = __vmaxu4(x, x >> 16);
+    x = max(x & 0xFFu, x >> 8 & 0xFFu);
+    return x == 0 || x == 255 ? kNothing : (int)x - 127;
+}
+// The scale of what is next, whose largest has exponent e.  Exponents of 120 and more in a scale would leave fp32.
+__device__ __forceinline__ int next_scale(int scale, int e, int low, int high, int best) {
+    if (e == kNothing || (e + scale >= low && e + scale <= high)) return scale;
+    return max(-120, min(120, best - e));
+}
+__device__ __forceinline__ int forward_scale(int scale, int e) { return next_scale(scale, e, -6, 5, 2); }
+__device__ __forceinline__ int gradient_scale(int scale, int e) { return next_scale(scale, e, -1, 6, 3); }
+__device__ __forceinline__ float power_of_two(int e) {     // e <= 127; 0 below fp32's normal numbers
+    return e < -126 ? 0.0f : __int_as_float((e + 127) << 23);
+}
+// x 2^e for |e| <= 252, without leaving fp32 on the way
+__device__ __forceinline__ float times_power(float x, int e) { return x * power_of_two(e / 2) * power_of_two(e - e / 2); }
 
 }  // namespace gdr
 
@@ -202,7 +226,6 @@ struct GdrGrads {         // the gradients that enter a backward pass
     const __nv_bfloat16* dout;        // [tokens][Hv][128]
     const void* dfinal;               // [N][Hv][128][128] or nullptr
     int dfinal_dtype;
-    unsigned* amax;                   // [N][Hk], 0 at first
 };
 
 struct GdrBackward {      // what the backward pass has besides
@@ -226,7 +249,7 @@ int gdr_bwd_chunk_split(const GdrBackward& P, int sms);
 cudaError_t launch_gdr_map(const GdrInputs& in, int* first, int* order, int* valid, int* err, cudaStream_t s);
 // `early`: may begin before the kernel before it has ended
 cudaError_t launch_gdr_prep(const GdrChunked& P, int sms, bool early, cudaStream_t s);
-cudaError_t launch_gdr_prep(const GdrBackward& P, int sms, cudaStream_t s);   // finds the largest gradients too
+cudaError_t launch_gdr_prep(const GdrBackward& P, int sms, cudaStream_t s);   // finds the largest |scale dO| too
 cudaError_t launch_gdr_chain(const GdrChunked& P, bool early, cudaStream_t s);
 
 }  // namespace kda

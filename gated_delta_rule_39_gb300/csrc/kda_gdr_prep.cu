@@ -118,7 +118,6 @@ struct PrepSmem {
     };
     float g[kC];                                           // running sum of g in base 2
     float b[kC];
-    unsigned top[kPrepThreads / 32];
 };
 
 // rows [0, 64) of one head, zeros from row `rows` on, into a tile of 256-byte rows
@@ -181,52 +180,19 @@ __device__ __forceinline__ void put_negative(float (*M)[kLd], int row, int col, 
     }
 }
 
-// Backward: the largest magnitude of the gradients that enter a (sequence, key head), by all its
-// chunks' CTAs: scale dO of the chunk's tokens and a share of the last state's gradient.
-__device__ __forceinline__ void largest_gradient(const GdrInputs& I, const GdrGrads& B, const Span& span, int n, int c, int hk,
-                                                 int part, int split, unsigned* shared_top, int tid) {
-    const int share = I.Hv / I.Hk, rows = min(kC, span.len - c * kC), units = share * 16;   // 16-byte units of a token
-    const __nv_bfloat16* src = B.dout + ((span.start + (long long)c * kC) * I.Hv + hk * share) * kDim;
-    const auto bits = [](unsigned u) {         // two bf16 values; NaN compares above infinity
-        return max(u & 0x7FFF0000u, (u & 0x7FFFu) << 16);
-    };
-    const auto four = [&](uint4 u) { return max(max(bits(u.x), bits(u.y)), max(bits(u.z), bits(u.w))); };
-    unsigned top = 0;
-    for (int at = 32 * part + (tid & 31); at < units; at += 32 * split) {
+// Backward: the biased exponent of the largest |scale dO| (not of NaN) in this warp's rows of a chunk and head
+__device__ __forceinline__ unsigned size_of_rows(const __nv_bfloat16* src, long long stride, int rows, float scale, int tid) {
+    uint4 u[kC * 16 / kPrepThreads];
+    src += (tid & 15) * 8;
 #pragma unroll
-        for (int i = 0; i < kC; i += 8 * (kPrepThreads / 32)) {
-            uint4 u[8];
+    for (int i = 0; i < kC * 16 / kPrepThreads; ++i)      // rows past the end repeat the last one
+        u[i] = __ldg(reinterpret_cast<const uint4*>(src + min((tid >> 4) + i * (kPrepThreads / 16), rows - 1) * stride));
+    __nv_bfloat162 top = __float2bfloat162_rn(0.0f);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int row = i + j * (kPrepThreads / 32) + (tid >> 5);
-                u[j] = __ldg(reinterpret_cast<const uint4*>(src + (size_t)min(row, rows - 1) * I.Hv * kDim + at * 8));
-            }
-#pragma unroll
-            for (int j = 0; j < 8; ++j) top = max(top, four(u[j]));
-        }
-    }
-    top = __float_as_uint(fabsf(I.scale) * __uint_as_float(top));
-    if (B.dfinal) {
-        const bool f32 = B.dfinal_dtype == KDA_F32;
-        const size_t base = ((size_t)n * I.Hv + hk * share) * kDim * kDim, count = (size_t)share * kDim * kDim;
-        const size_t per = f32 ? 4 : 8;        // values of 16 bytes
-        const size_t step = (size_t)((span.len + kC - 1) / kC) * split * kPrepThreads;
-        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const unsigned char*>(B.dfinal) + base * (16 / per));
-        for (size_t i = ((size_t)c * split + part) * kPrepThreads + tid; i < count / per; i += 8 * step) {
-            uint4 u[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) u[j] = i + j * step < count / per ? __ldg(src + i + j * step) : make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                top = max(top, f32 ? max(max(u[j].x & 0x7FFFFFFFu, u[j].y & 0x7FFFFFFFu), max(u[j].z & 0x7FFFFFFFu, u[j].w & 0x7FFFFFFFu))
-                                   : four(u[j]));
-        }
-    }
-    top = __reduce_max_sync(0xFFFFFFFFu, top);
-    if ((tid & 31) == 0) shared_top[tid >> 5] = top;
-    __syncthreads();
-    // a maximum does not depend on the order of the atomics
-    if (tid == 0) atomicMax(&B.amax[(size_t)n * I.Hk + hk], max(max(shared_top[0], shared_top[1]), max(shared_top[2], shared_top[3])));
+    for (int i = 0; i < kC * 16 / kPrepThreads; ++i)
+        for (const uint32_t x : {u[i].x, u[i].y, u[i].z, u[i].w}) top = __hmax2(top, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&x)));
+    const float2 f = __bfloat1622float2(top);
+    return __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(fabsf(scale) * fmaxf(f.x, f.y))) >> 23;
 }
 
 template <bool kGrads, bool kSplit>
@@ -268,7 +234,11 @@ __global__ void __launch_bounds__(kPrepThreads, kPrepPerSm) gdr_prep_kernel(GdrC
         }
     };
     fetch_gates(hk * share + part);
-    if (kGrads) largest_gradient(I, B, span, n, c, hk, part, split, S.top, tid);
+    if (kGrads)                        // for the scales of the gradient's chain, while the rows are on their way
+        for (int h = hk * share + part; h < (hk + 1) * share; h += split) {
+            const unsigned x = size_of_rows(B.dout + (tok * I.Hv + h) * kDim, (long long)I.Hv * kDim, rows, I.scale, tid);
+            if (lane == 0) (P.blocks + ((size_t)chunk * I.Hv + h) * kBlockBytes + 2 * kTileBytes + 4 * kGateDo)[tid >> 5] = (unsigned char)x;
+        }
     cp_async_wait<0>();
     __syncthreads();
     // rows 16 w ..  of K K^T and Q K^T, columns 0 .. 16 w + 15

@@ -119,6 +119,53 @@ __device__ __forceinline__ void scale32(uint32_t (&x)[32], float d) {
         asm("mov.b64 {%0, %1}, %2;" : "=r"(x[i]), "=r"(x[i + 1]) : "l"(v));
     }
 }
+// ---- scales ----------------------------------------------------------------------------------
+// One warp of a chain chooses the scales; the others find the factors that they need here.  Entry i % 4
+// is chunk i's (as the chain walks); what is published before chunk i is at i % 4 too.
+struct ScaleRing {
+    int top[4][kStateWarps];                  // exponents of each state warp's largest
+    float ratio[4];                           // of a chunk's scale to the one before
+    float in[4], out[4];                      // scale 2^scale, for dO; scale 2^-scale or 2^-scale, for results
+};
+// the largest exponent that the state warps published, in a scale, before chunk i
+__device__ __forceinline__ int published(const ScaleRing& R, int i, int scale) {
+    int e = kNothing;
+#pragma unroll
+    for (int w = 0; w < kStateWarps; ++w) e = max(e, R.top[i & 3][w]);
+    return e == kNothing ? kNothing : e - scale;
+}
+// The exponents of the state warps' largest, each warp's at its place.  Of a state,
+__device__ __forceinline__ void publish(int& top, float largest, int lane) {
+    const int e = exponent_of(__uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(largest))));
+    if (lane == 0) top = e;
+}
+__device__ __forceinline__ void publish(int& top, const uint32_t (&x)[2][32], int lane) {
+    float m[4] = {};
+#pragma unroll
+    for (int i = 0; i < 64; ++i) m[i & 3] = fmaxf(m[i & 3], fabsf(__uint_as_float(x[i >> 5][i & 31])));
+    publish(top, fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])), lane);
+}
+// and, a chunk on, of d times one that is held as fp16 pairs, in the chunk's scale
+__device__ __forceinline__ void publish(int& top, const uint32_t (&f)[2][16], float d, int lane) {
+    __half2 m[2] = {__float2half2_rn(0.0f), __float2half2_rn(0.0f)};
+#pragma unroll
+    for (int i = 0; i < 32; ++i) m[i & 1] = __hmax2(m[i & 1], __habs2(*reinterpret_cast<const __half2*>(&f[i >> 4][i & 15])));
+    const float2 y = __half22float2(__hmax2(m[0], m[1]));
+    publish(top, d * fmaxf(y.x, y.y), lane);
+}
+// A state warp's part of a state in tensor memory times `by`: through other registers than the ones that the chain
+// keeps it in, whose moves around a branch would cost every chunk 330 cycles.
+__device__ __forceinline__ void rescale(uint32_t taddr, float by) {
+#pragma unroll 1
+    for (int i = 0; i < 2; ++i) {
+        uint32_t y[32];
+        tc::ld32(taddr + 32 * i, y);
+        tc::wait_ld();
+        scale32(y, by);
+        tc::st32(taddr + 32 * i, y);
+    }
+    tc::wait_st();
+}
 // two bf16 values times `by`, as fp16
 __device__ __forceinline__ uint32_t scaled_half2(uint32_t u, unsigned long long by) {
     unsigned long long v;
@@ -181,13 +228,33 @@ __device__ __forceinline__ void store_tokens(__nv_bfloat16* out, size_t step, in
     }
 }
 
-__device__ __forceinline__ float load_state(const void* p, int dtype, size_t i) {
-    return dtype == KDA_F32 ? static_cast<const float*>(p)[i]
-                            : __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
+// A state warp's part of a state in memory: 64 rows of its lane's column, from element `at` on.  (One
+// branch on the type, so that all loads are on their way together; nullptr: zeros.)
+__device__ __forceinline__ void load_state(uint32_t (&x)[2][32], const void* p, int dtype, size_t at) {
+    if (!p) {
+#pragma unroll
+        for (int i = 0; i < 64; ++i) x[i >> 5][i & 31] = 0u;
+    } else if (dtype == KDA_F32) {
+        const uint32_t* s = static_cast<const uint32_t*>(p) + at;
+#pragma unroll
+        for (int i = 0; i < 64; ++i) x[i >> 5][i & 31] = s[i * kDim];
+    } else {
+        const uint16_t* s = static_cast<const uint16_t*>(p) + at;
+#pragma unroll
+        for (int i = 0; i < 64; ++i) x[i >> 5][i & 31] = (uint32_t)s[i * kDim] << 16;
+    }
 }
-__device__ __forceinline__ void store_state(void* p, int dtype, size_t i, float x) {
-    if (dtype == KDA_F32) static_cast<float*>(p)[i] = x;
-    else static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(x);
+// the same to memory, times `by`
+__device__ __forceinline__ void store_state(const uint32_t (&x)[2][32], float by, void* p, int dtype, size_t at) {
+    if (dtype == KDA_F32) {
+        float* s = static_cast<float*>(p) + at;
+#pragma unroll
+        for (int i = 0; i < 64; ++i) s[i * kDim] = by * __uint_as_float(x[i >> 5][i & 31]);
+    } else {
+        __nv_bfloat16* s = static_cast<__nv_bfloat16*>(p) + at;
+#pragma unroll
+        for (int i = 0; i < 64; ++i) s[i * kDim] = __float2bfloat16_rn(by * __uint_as_float(x[i >> 5][i & 31]));
+    }
 }
 
 }  // namespace gdr

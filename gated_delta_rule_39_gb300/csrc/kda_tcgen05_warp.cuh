@@ -54,6 +54,12 @@ __device__ __forceinline__ void commit_on(uint32_t mbar_smem, uint32_t on) {
         " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n"
         ::"r"(mbar_smem), "r"(on) : "memory");
 }
+// an arrival of the thread that `on` picks, beside its commit
+__device__ __forceinline__ void arrive_on(uint32_t mbar_smem, uint32_t on) {
+    asm volatile(
+        "{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n @q mbarrier.arrive.shared::cta.b64 _, [%0];\n}\n"
+        ::"r"(mbar_smem), "r"(on) : "memory");
+}
 // 16 lanes x 32 columns as accumulator fragments of mma.sync: registers 4 j .. of a thread are
 // (lane / 4, 8 j + 2 (lane % 4)), the column after it, and both 8 lanes further down
 __device__ __forceinline__ void ld_fragments(uint32_t taddr, uint32_t (&r)[16]) {

@@ -417,8 +417,15 @@ int kda_qk_norm_bwd(const void* q, const void* k, const void* dq_out, const void
  *               key channel, or NULL; a malformed cu_seqlens writes nothing
  *   B >= 1, T >= 0, K = V = 128
  *
- * The state is carried in fp32; the tensor-core products have fp16 operands, so q, k, v and
- * the states have to stay below 65,504 in magnitude.  Takes about 0.3 KB of scratch per
+ * The state is carried in fp32; the tensor-core products have fp16 operands.  Values and states of any
+ * size keep their accuracy: every chunk of 64 tokens works on them times a power of two of its own.
+ * What is smaller than 2^-14 of the largest value or state in its chunk, or of the values of the chunk
+ * before, is held to 2^-25 of that largest.  Queries and keys are taken as they are: they, q.k and
+ * the products of their decays have to stay below 65,504 in magnitude, and entries below 2^-14 are
+ * held to 2^-25 (unit vectors, as kda_qk_norm makes them, are well inside); beta is held to 2^-25, too.
+ * g above 0 (growth) is not refused, but e^g summed over a chunk has to stay in that range.
+ * A token that is not finite makes its sequence not finite from its chunk on, tokens before
+ * it in that chunk included.  Takes about 0.3 KB of scratch per
  * token and value head from the stream-ordered allocator.  Deterministic.  (Without
  * cu_seqlens, T <= 8 with more sequences times heads than the GPU has SMs is computed token
  * by token in fp32 and takes no scratch.)
@@ -441,9 +448,11 @@ int kda_gdr_fwd(const void* q, const void* k, const void* v, const void* g, cons
  *   d_initial_state  [N, Hv, 128, 128] of d_initial_state_dtype, or NULL (not written)
  *
  * The forward pass's states are formed again.  Accuracy is that of fp16 operands with fp32
- * sums, whatever the gates' type: the incoming gradients are scaled per (sequence, key head)
- * by the power of two that brings the largest to 16 .. 32, so gradients of any size keep it;
- * q, k, v and the states have to stay below 65,504 as in kda_gdr_fwd.  Deterministic.
+ * sums, whatever the gates' type.  Gradients of any size keep it, and so do values and states: each
+ * chunk works on either times a power of two of its own, as in kda_gdr_fwd; gradients that decay
+ * by more than 2^-14 inside a chunk lose bits there.  From chunk to chunk the gradient of the state may
+ * grow by what 64 tokens add with q and k of about unit length (up to 2.6).  The range of q, k and beta is that of
+ * kda_gdr_fwd.  Deterministic.
  * Scratch: kda_gdr_bwd_workspace_bytes() from the stream-ordered allocator (about 1.9 KB per
  * token and value head).
  */
