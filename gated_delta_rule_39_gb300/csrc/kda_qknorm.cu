@@ -703,7 +703,6 @@ int kda_qk_norm_bwd(const void* q, const void* k, const void* dq_out, const void
     if (T > 0 && (!dq_out || (Hk && !dk_out))) return KDA_ERR_NULL;
     if ((q_weight != nullptr) != (dq_weight != nullptr) || (k_weight != nullptr) != (dk_weight != nullptr))
         return KDA_ERR_NULL;
-    if (!Hk && dk_weight) return KDA_ERR_SHAPE;
     const size_t size = dtype == KDA_BF16 ? 2 : 4;
     for (const void* p : {dq_out, dk_out})
         if (reinterpret_cast<uintptr_t>(p) % size) return KDA_ERR_ALIGN;

@@ -393,7 +393,8 @@ int kda_qk_norm(const void* q, const void* k, void* q_out, void* k_out, int dtyp
  *   dq_out, dk_out  dL/d(q_out), dL/d(k_out): [T, Hq, D], [T, Hk, D] of dtype, contiguous
  *   dq, dk          dL/dq, dL/dk of dtype, contiguous
  *   dq_weight, dk_weight  fp32 [D], required with the weight and NULL without it; summed
- *               over tokens and heads in a fixed order (results are deterministic)
+ *               over tokens and heads in a fixed order (results are deterministic); zeros where
+ *               there are none (T = 0, or Hk = 0)
  * Other arguments as kda_qk_norm.  With weights it takes a few hundred KB of scratch from the
  * stream-ordered allocator.
  */
