@@ -149,14 +149,15 @@ bool capturing(cudaStream_t s) {
 
 // How many chunks of one long sequence to prepare before its chains begin; the rest are prepared
 // beside them, on the SMs that the chains (one per value head) leave.  0: not worth it, or the stream is
-// being captured.  A chain takes 1.6 us per chunk and the whole GPU 0.0122 us to prepare a chunk of a
+// being captured.  A chain takes 1.7 us per chunk and the whole GPU 0.0122 us to prepare a chunk of a
 // head, so while a chain walks a chunk the idle SMs prepare `rate` of them; of two parts the first is 1
-// in 1 + rate.  (8,192 tokens: 96 heads 359 -> 337 us, 64 heads 303 -> 273, 32 heads 240 -> 225.)
+// in 1 + rate.  (Times of this GPU: others would cost some overlap, no result.  8,192 tokens: 96 heads 373 -> 343
+// us, 64 heads 321 -> 283, 32 heads 268 -> 245.)
 int chunks_before(const GdrChunked& P, int sms, cudaStream_t s) {
     const int units = P.in.Hv, chunks = P.chunks.total;
     if (P.in.cu || P.in.N != 1 || chunks < 64 || (long long)chunks * units < 2500 || units >= sms - sms / 8) return 0;
     if (capturing(s)) return 0;
-    const float rate = 1.6f / 0.0122f * (float)(sms - units) / ((float)units * (float)sms);
+    const float rate = 1.7f / 0.0122f * (float)(sms - units) / ((float)units * (float)sms);
     return std::max(8, (int)std::ceil((float)chunks / (1.0f + rate)));
 }
 
@@ -245,8 +246,8 @@ bool in_two_parts(const GdrInputs& in, int chunks, int sms) {
 // and how many chunks at its end to have the gradient's chain walk first, so that the chunk kernel
 // can take them beside the rest of the chain, on the SMs that it leaves.  The gradient's chain takes 2.4
 // us per chunk, the one for the states, which has to be over by then, 1.6, and the chunk kernel on the
-// whole GPU 0.073 us per chunk and head.  (4,096 tokens: 32 heads 343 -> 329 us, 16 heads 267 -> 240; 8,192
-// tokens, 8 heads: 406 -> 355.)
+// whole GPU 0.073 us per chunk and head (times of this GPU; the ones measured last, 2.45, 1.7 and 0.076, choose no
+// better).  (4,096 tokens: 32 heads 354 -> 326 us, 16 heads 270 -> 240; 8,192 tokens, 8 heads: 410 -> 357.)
 int chunks_first(const GdrBackward& B, int sms, cudaStream_t s) {
     const int units = B.fwd.in.Hv, chunks = B.fwd.chunks.total;
     if (!in_two_parts(B.fwd.in, chunks, sms)) return 0;

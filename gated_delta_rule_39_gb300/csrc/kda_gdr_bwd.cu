@@ -43,8 +43,8 @@ using namespace gdr;
 // fewer pairs than SMs (kSplit), a cluster shares a pair's value heads and adds dQ and dK up,
 // in the order of its CTAs (512 tokens x 8 heads on 4 key heads: 15 us, 25 without).
 //
-// Measured: 4,096 tokens x 32 heads 147 us, 11 us per head and SM; 61 % of the cycles move shared
-// memory (operands of mma.sync, read again by every warp that needs them) and 0.37 of the issue
+// Measured: 4,096 tokens x 32 heads 155 us, 11.5 us per head and SM; 60 % of the cycles move shared
+// memory (operands of mma.sync, read again by every warp that needs them) and 0.40 of the issue
 // slots are taken.
 constexpr int kChunkThreads = 512, kParts = kChunkThreads / 128;
 

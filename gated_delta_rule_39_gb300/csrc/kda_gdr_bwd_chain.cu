@@ -15,8 +15,8 @@
 // memory (channels contiguous: MN-major) and are off the chain.  The state warps also write
 // DS16 and Y16 of every chunk to memory; four warps write dV = beta Y.
 //
-// Measured: 2.4 us per chunk (4,096 tokens x 32 heads: 152 us); without those 48 KB to memory it
-// would be 2.0, without dV 2.1: the stores share the load/store unit with the conversions.
+// Measured: 2.4 us per chunk (4,096 tokens x 32 heads: 157 us, 153 with scales left out); without those 48 KB to
+// memory it would be 2.0, without dV 2.1: the stores share the load/store unit with the conversions.
 #include "kda_gdr_chain.cuh"
 
 namespace kda {

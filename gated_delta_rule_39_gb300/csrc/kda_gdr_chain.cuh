@@ -22,11 +22,11 @@
 // 4 warps bring in keys, values, T and P of the next chunks, 4 the queries, 4 write the
 // outputs, one chooses the scales and two find out how large the values are.  Every role's loop is kept small: with the MMAs issued from a state warp, the
 // others' jumps over that code cost 200 cycles each (instruction cache misses).
-// Measured: 1.6 us per chunk of 64 tokens (8,192 tokens x 96 heads on 96 SMs: 204 us; the same
-// chain with mma.sync and a warp per 16 channels took 645).  Of some 3,000 cycles the tensor core runs
+// Measured: 1.7 us per chunk of 64 tokens (8,192 tokens x 96 heads on 96 SMs: 220 us, 204 with scales left out; the
+// same chain with mma.sync and a warp per 16 channels took 645).  Of some 3,200 cycles the tensor core runs
 // 1,200; the rest are the three roundings (100 to 350 cycles each), the hand-overs (130 to 190
-// cycles from a warp's arrival to the MMA, as many back) and their contention with the
-// other roles (0.46 of the issue slots are taken).
+// cycles from a warp's arrival to the MMA, as many back), the look for a new scale (some 120) and their contention
+// with the other roles (0.47 of the issue slots are taken).
 // All waits are bounded: a role whose wait gives up returns, and so do those that wait for it.
 #pragma once
 

@@ -92,14 +92,14 @@ __global__ void __launch_bounds__(kMapThreads) gdr_map_kernel(GdrInputs I, int* 
 // ---- prep -------------------------------------------------------------------------------
 // One CTA of 4 warps per (chunk, query/key head), or `split` of them that share the value heads
 // where all are on the GPU at once.  Warp w forms rows 16 w .. 16 w + 15 of
-// K K^T and Q K^T on tensor cores (bf16 data, fp32 sums; kept in registers for all value
+// K K^T and Q K^T with mma.sync (bf16 data, fp32 sums; kept in registers for all value
 // heads of the group), and per value head: the gates' running sum, A and P, and
 // T = (I + A)^-1: the four 16 x 16 diagonal blocks by forward substitution in fp32 (a lane
 // owns a column), then T21 = -T22 A21 T11 for blocks of 16 and of 32 with tf32 products.  T
 // takes A's place block by block.
 //
 // Five CTAs share an SM to cover each other's chains of small steps: A, T and P live where K and Q
-// were.  Measured: 8,192 tokens x 96 heads 150 us, 4.1 TB/s (K and Q once, 17 KB out per chunk and
+// were.  Measured: 8,192 tokens x 96 heads 155 us, 4.0 TB/s (K and Q once, 17 KB out per chunk and
 // head): 72 % of the cycles move shared memory, which the fp32 tile's small products read in 4-byte
 // pieces, and the waits between them take most of the rest.
 constexpr int kPrepThreads = 128, kPrepPerSm = 5;

@@ -36,7 +36,9 @@ constexpr int kManyHeads = 8;             // of a token, at most, for a group th
 // angles, weights and the weights' gradients add as many each).  Forwards:
 __host__ __device__ constexpr int fwd_per_sm(int vec, int ns) { return vec * ns <= 2 ? 3 : 2; }
 // Backwards, three where 80 registers are enough (bf16, 16,384 x 64 heads without angles and weights 123
-// us, with two blocks 141); with angles and weights on 16-byte accesses three would spill.
+// us, with two blocks 141).  Even the 128 of two blocks are not enough where the weights' sums are largest: bf16 with
+// weights and angles on 16-byte accesses spills 48 bytes, fp32 with weights and two slots 60 (with angles 190), single
+// elements with eight slots 44 to 184 (8 with angles alone).
 __host__ __device__ constexpr int bwd_per_sm(int vec, int ns, bool rot, bool w) {
     return vec * ns <= 2 || (vec * ns <= 4 && !w) || (vec == 8 && !rot && !w) ? 3 : 2;
 }
