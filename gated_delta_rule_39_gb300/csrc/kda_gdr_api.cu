@@ -290,6 +290,7 @@ cudaError_t run_backward(const GdrBackward& B, int last, float* carry, int sms, 
     GdrBackward a = part_of(B, 0, first), b = part_of(B, first, last);
     a.in.dfinal = b.dinit = carry;
     a.in.dfinal_dtype = b.dinit_dtype = KDA_F32;
+    if (!b.fwd.init_state) b.fwd.init_state = carry;       // (not read) its first chunk has a state before it
     Fork fork(s);
     cudaError_t e = fork.make();
     if (e == cudaSuccess) e = chain(b, &B.fwd);

@@ -124,6 +124,7 @@ __device__ __forceinline__ void bulk_prefetch(const void* p, int bytes) {
 struct Place {
     int chunk, hk, rows, n;
     long long tok;            // the chunk's first token
+    bool from_zero;           // its state before is zero: a sequence's first chunk, without an initial state
 };
 __device__ __forceinline__ bool place(const GdrChunked& P, int pair, Place& p) {
     const GdrInputs& I = P.in;
@@ -135,6 +136,7 @@ __device__ __forceinline__ bool place(const GdrChunked& P, int pair, Place& p) {
     const Span span = span_of(I, P.chunks, p.n);
     p.tok = span.start + (long long)c * kC;
     p.rows = min(kC, span.len - c * kC);
+    p.from_zero = c == 0 && !P.init_state;
     return true;
 }
 
@@ -569,6 +571,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) gdr_bwd_chunk_kernel(GdrBack
                     const float y = __shfl_down_sync(0xFFFFFFFFu, x, o);
                     if (lane + o < 32) x += y;
                 }
+                if (now.from_zero && lane == 0) x = 0.0f;      // the first token has nothing to forget: else sums that cancel
                 if (2 * lane < rows) store_gate(B.dg, I.gate_dtype, (size_t)(tok + 2 * lane) * I.Hv + h, times_power(x, -held));
                 if (2 * lane + 1 < rows)
                     store_gate(B.dg, I.gate_dtype, (size_t)(tok + 2 * lane + 1) * I.Hv + h, times_power(x - dgv[0], -held));
