@@ -15,17 +15,19 @@
 // exact), so that between two products the state warps only round an accumulator.  V, R, X and S stand for
 // 2^scale times themselves (kda_gdr_chunk.cuh): the identity's ones are 2^scale, the state is multiplied
 // when the scale changes, and the outputs are multiplied back.  Chunk c's scale comes from e^GC S as chunk c - 1
-// began, and the values of both, so that it is known before chunk c's first product.
+// began, and the values of both, so that it is known before chunk c's first product.  S is looked at every kLookEvery
+// chunks, and wherever what remains of it after the decays may be far above the values; else its size is
+// taken to follow both.
 //
 // Warps: 8 state warps (lane quarter w % 4, half of the columns each) do that rounding; one
 // warp issues the MMAs, those that the chain does not need behind the state's update;
 // 4 warps bring in keys, values, T and P of the next chunks, 4 the queries, 4 write the
 // outputs, one chooses the scales and two find out how large the values are.  Every role's loop is kept small: with the MMAs issued from a state warp, the
 // others' jumps over that code cost 200 cycles each (instruction cache misses).
-// Measured: 1.7 us per chunk of 64 tokens (8,192 tokens x 96 heads on 96 SMs: 220 us, 204 with scales left out; the
-// same chain with mma.sync and a warp per 16 channels took 645).  Of some 3,200 cycles the tensor core runs
+// Measured: 1.65 us per chunk of 64 tokens (8,192 tokens x 96 heads on 96 SMs: 213 us, 204 with scales left out; the
+// same chain with mma.sync and a warp per 16 channels took 645).  Of some 3,100 cycles the tensor core runs
 // 1,200; the rest are the three roundings (100 to 350 cycles each), the hand-overs (130 to 190
-// cycles from a warp's arrival to the MMA, as many back), the look for a new scale (some 120) and their contention
+// cycles from a warp's arrival to the MMA, as many back) and their contention
 // with the other roles (0.47 of the issue slots are taken).
 // All waits are bounded: a role whose wait gives up returns, and so do those that wait for it.
 #pragma once
@@ -39,6 +41,9 @@ namespace gdr {
 namespace chain {
 
 constexpr int kStages = 3;                    // chunks in shared memory
+// A look at the state takes issue slots where the chain waits for them: with one in every chunk 20,000 tokens x 8 heads take
+// 484 us, in every 4th 476, in every 8th 473.
+constexpr int kLookEvery = 4, kFarAbove = 8;  // (2^8)
 constexpr int kOutWarps = 4;
 constexpr int kFirstKeys = kStateWarps + kOutWarps, kFirstQueries = kFirstKeys + kProducers / 32,
               kMmaWarp = kFirstQueries + kProducers / 32;
@@ -64,7 +69,7 @@ struct ChainSmem {
     uint64_t acc, x, s_done;                  // products done
     uint64_t q_full, o_done[2], o_free[2];
     uint64_t done, drain;
-    uint64_t begun, ready;                    // the initial state's exponents, chunk 0's scale are there
+    uint64_t begun, tops, ready;              // the initial state's exponents, a chunk's, chunk 0's scale are there
     uint64_t sized[kStages];
     float largest[kStages][2];                // |V| of the halves of a stage's values
     ScaleRing scales;                         // published: of the initial state, then of e^GC S of the chunk before
@@ -206,7 +211,6 @@ __device__ void issue(const GdrChunked& P, ChainSmem& S, int nch, uint32_t tmem)
         if (!wait(S.x16, turn)) return;
         product_mn(tmem + kTmS, tmem + kTmX16, stage + offsetof(ChainSmem::Stage, kd), kId128, true, on);
         tc::commit_on(smem_u32(&S.s_done), on);
-        tc::arrive_on(smem_u32(&S.s_done), on);  // hands on the next scale, too
         if (!kSave) {                         // outputs
             const uint32_t o = tmem + kTmO + 64 * uniform(turn);
             product_k<8>(o, s16, smem_u32(S.q), kId64, false, on);
@@ -241,6 +245,7 @@ __device__ void states(const GdrChunked& P, ChainSmem& S, const Span& span, int 
         scale32(x[0], S.scales.ratio[0]);
         scale32(x[1], S.scales.ratio[0]);
     }
+    int look = 0;
 #pragma unroll 1
     for (int c = 0; c < nch; ++c) {
         const unsigned turn = (unsigned)(c & 1);
@@ -261,7 +266,10 @@ __device__ void states(const GdrChunked& P, ChainSmem& S, const Span& span, int 
             keep_units(P.states + unit * kStateTile, v, 8 * half, f[0]);
             keep_units(P.states + unit * kStateTile, v, 8 * half + 4, f[1]);
         }
-        publish(S.scales.top[(c + 1) & 3][w], f, d, lane);
+        if (look) {
+            publish(S.scales.top[(c + 1) & 3][w], f, d, lane);
+            if (lane == 0) bar_arrive(&S.tops);
+        }
         uint32_t y[32];
         if (!bar_wait(&S.acc, turn, P.err)) return;
         tc::fence_after_sync();
@@ -279,10 +287,11 @@ __device__ void states(const GdrChunked& P, ChainSmem& S, const Span& span, int 
         operand_ready(&S.x16, lane);
         if (kSave) keep_units(P.xs + unit * kTokenTile, v, 4 * half, f[0]);
         d = next_d;
+        const float ratio = c + 1 < nch ? S.scales.ratio[(c + 1) & 3] : 1.0f;     // there since X is
+        look = S.scales.look[(c + 1) & 3];
         if (!bar_wait(&S.s_done, turn, P.err)) return;
         tc::fence_after_sync();
-        const float ratio = S.scales.ratio[(c + 1) & 3];
-        if (__builtin_expect(c + 1 < nch && ratio != 1.0f, 0)) rescale(tl + kTmS + 64 * half, ratio);
+        if (__builtin_expect(ratio != 1.0f, 0)) rescale(tl + kTmS + 64 * half, ratio);
         tc::ld32(tl + kTmS + 64 * half, x[0]);
         tc::ld32(tl + kTmS + 64 * half + 32, x[1]);
         tc::wait_ld();
@@ -291,15 +300,16 @@ __device__ void states(const GdrChunked& P, ChainSmem& S, const Span& span, int 
 }
 
 // ---- sizes of the values (two warps, half a tile each) -------------------------------------------
-// They run ahead of the scales, but a stage is not given back before the scale warp's arrival for its chunk, which
-// comes after theirs: so neither the values nor a stage's barrier change while someone still needs them.
-__device__ inline void sizes(const GdrChunked& P, ChainSmem& S, int nch, int half, int lane) {
+// They run ahead of the scales, but a stage is not given back before the scale warp's arrival for its chunk (with X),
+// which comes after theirs: so neither the values nor a stage's barrier change while someone still needs them.
+__device__ inline void sizes(const GdrChunked& P, ChainSmem& S, const Span& span, int nch, int half, int lane) {
 #pragma unroll 1
     for (int c = 0; c < nch; ++c) {
         const int st = c % kStages;
         const unsigned char* tile = S.stage[st].v + half * kHalfTile + 16 * lane;
         const unsigned phase = (unsigned)((c / kStages) & 1);
-        if (!bar_wait(&S.copied[st], phase, P.err) || !bar_wait(&S.full[st], phase, P.err)) return;
+        // whole tiles are copied, the last one's rows stored by the warps that bring in the keys
+        if (!bar_wait(span.len - c * kC >= kC ? &S.copied[st] : &S.full[st], phase, P.err)) return;
         __nv_bfloat162 top[4] = {};
 #pragma unroll 4
         for (int i = 0; i < kHalfTile; i += 16 * 32) {
@@ -318,8 +328,8 @@ __device__ inline void sizes(const GdrChunked& P, ChainSmem& S, int nch, int hal
 }
 
 // ---- scales (one warp) ------------------------------------------------------------------------
-// Chunk c + 1's while chunk c's X is formed: what the state warps publish is there with R16, and X16's
-// barrier hands the choice to the issuing warp, with the identity as the next chunk wants it.
+// Chunk c + 1's while chunk c's R and X are formed; X's barrier hands the choice to the state warps (and X16's on to the
+// issuing warp, with the identity as the next chunk wants it).
 template <bool kSave>
 __device__ void scales(const GdrChunked& P, ChainSmem& S, const Span& span, int nch, int h, int lane) {
     float* gates = reinterpret_cast<float*>(P.blocks + ((size_t)span.chunk * P.in.Hv + h) * kBlockBytes + 2 * kTileBytes);
@@ -344,7 +354,10 @@ __device__ void scales(const GdrChunked& P, ChainSmem& S, const Span& span, int 
     };
     int v, next_v = kNothing;
     if (!values(0, v) || (P.init_state && !bar_wait(&S.begun, 0u, P.err))) return;
-    int scale = forward_scale(0, max(published(S.scales, 0, 0), v));
+    int size = published(S.scales, 0, 0);     // exponent of the state as a chunk begins
+    int scale = forward_scale(0, max(size, v)), look = 0;
+    unsigned looks = 0;
+    float d = gates[kGateAll];
     if (scale) identity(scale);
     set(0, scale, 0);
     __syncwarp();
@@ -352,16 +365,31 @@ __device__ void scales(const GdrChunked& P, ChainSmem& S, const Span& span, int 
 #pragma unroll 1
     for (int c = 0; c < nch; ++c) {
         if (c + 1 < nch && !values(c + 1, next_v)) return;
-        if (!bar_wait(&S.r16, (unsigned)(c & 1), P.err)) return;
+        const float next_d = c + 1 < nch ? gates[(c + 1) * step + kGateAll] : 0.0f;
+        size = max(size + exponent_of(d), kNothing);
+        d = next_d;
+        if (look) {
+            if (!bar_wait(&S.tops, looks++ & 1, P.err)) return;
+            size = published(S.scales, c + 1, scale);
+        }
+        size = max(size, v);
         if (c + 1 < nch) {
-            const int next = forward_scale(scale, max(published(S.scales, c + 1, scale), max(v, next_v)));
+            const int next = forward_scale(scale, max(size, next_v));
+            look = (c + 1) % kLookEvery == 0 || size > next_v + kFarAbove;
+            if (lane == 0) S.scales.look[(c + 1) & 3] = look;
             v = next_v;
-            if (next != scale) identity(next);        // R is there: the last product with the identity is over
+            if (next != scale) {
+                if (!bar_wait(&S.acc, (unsigned)(c & 1), P.err)) return;      // the last product with the identity is over
+                identity(next);
+            }
             set(c + 1, next, scale);
             scale = next;
         }
         __syncwarp();
-        if (lane == 0) bar_arrive(&S.x16);
+        if (lane == 0) bar_arrive(&S.x);
+        // no further than X: one arrival a phase, and what is written for chunk c + 2 takes the place of chunk c - 2's, whose
+        // outputs the issuing warp has seen read before X
+        if (!bar_wait(&S.x, (unsigned)(c & 1), P.err)) return;
     }
 }
 
@@ -402,10 +430,9 @@ __device__ __forceinline__ void run(const GdrChunked& P, const CUtensorMap& vmap
             bar_init(&S.empty[i], 1);
             bar_init(&S.sized[i], 2);
         }
-        for (uint64_t* b : {&S.acc, &S.x, &S.drain, &S.ready}) bar_init(b, 1);
-        bar_init(&S.s_done, 2);
-        for (uint64_t* b : {&S.s16, &S.r16, &S.begun}) bar_init(b, kStateWarps);
-        bar_init(&S.x16, kStateWarps + 1);
+        for (uint64_t* b : {&S.acc, &S.s_done, &S.drain, &S.ready}) bar_init(b, 1);
+        bar_init(&S.x, 2);                    // the product and the next scale
+        for (uint64_t* b : {&S.s16, &S.r16, &S.x16, &S.begun, &S.tops}) bar_init(b, kStateWarps);
         for (int i = 0; i < 2; ++i) bar_init(&S.o_done[i], 2);
         bar_init(&S.q_full, kProducers / 32);
         for (int i = 0; i < 2; ++i) bar_init(&S.o_free[i], kOutWarps);
@@ -450,7 +477,7 @@ __device__ __forceinline__ void run(const GdrChunked& P, const CUtensorMap& vmap
             if (w == kScaleWarp) {
                 if (nch > 0) scales<kSave>(P, S, span, nch, h, lane);
             } else {
-                sizes(P, S, nch, w - kScaleWarp - 1, lane);
+                sizes(P, S, span, nch, w - kScaleWarp - 1, lane);
             }
             return;
         }

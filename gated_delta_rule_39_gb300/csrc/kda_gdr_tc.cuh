@@ -125,7 +125,8 @@ __device__ __forceinline__ void scale32(uint32_t (&x)[32], float d) {
 struct ScaleRing {
     int top[4][kStateWarps];                  // exponents of each state warp's largest
     float ratio[4];                           // of a chunk's scale to the one before
-    float in[4], out[4];                      // scale 2^scale, for dO; scale 2^-scale or 2^-scale, for results
+    float in[4], out[4];                      // backwards `scale` 2^scale, for dO; 2^-scale, for results
+    int look[4];                              // forwards: whether the state's size is to be published in a chunk
 };
 // the largest exponent that the state warps published, in a scale, before chunk i
 __device__ __forceinline__ int published(const ScaleRing& R, int i, int scale) {
