@@ -240,7 +240,7 @@ __device__ void back_states(const GdrBackward& B, BackSmem& S, const Span& span,
         const size_t unit = (size_t)(span.chunk + c) * P.in.Hv + h;
         keep_units(B.dstates + unit * kStateTile, v, 8 * half, f[0]);
         keep_units(B.dstates + unit * kStateTile, v, 8 * half + 4, f[1]);
-        publish(S.scales.top[(i + 1) & 3][w], f, d, lane);
+        publish(S.scales.top[(i + 1) & 3][w], tl + kTmS16 + 32 * half, d, lane);
         uint32_t y[32];
         if (!bar_wait(&S.acc, turn, P.err)) return;
         tc::fence_after_sync();

@@ -267,7 +267,7 @@ __device__ void states(const GdrChunked& P, ChainSmem& S, const Span& span, int 
             keep_units(P.states + unit * kStateTile, v, 8 * half + 4, f[1]);
         }
         if (look) {
-            publish(S.scales.top[(c + 1) & 3][w], f, d, lane);
+            publish(S.scales.top[(c + 1) & 3][w], tl + kTmS16 + 64 * turn + 32 * half, d, lane);
             if (lane == 0) bar_arrive(&S.tops);
         }
         uint32_t y[32];

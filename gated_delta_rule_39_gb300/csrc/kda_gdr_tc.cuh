@@ -146,11 +146,15 @@ __device__ __forceinline__ void publish(int& top, const uint32_t (&x)[2][32], in
     for (int i = 0; i < 64; ++i) m[i & 3] = fmaxf(m[i & 3], fabsf(__uint_as_float(x[i >> 5][i & 31])));
     publish(top, fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])), lane);
 }
-// and, a chunk on, of d times one that is held as fp16 pairs, in the chunk's scale
-__device__ __forceinline__ void publish(int& top, const uint32_t (&f)[2][16], float d, int lane) {
+// and, a chunk on, of d times one whose fp16 pairs are in tensor memory, in the chunk's scale.  (Read again from
+// there: kept in registers for this, they cost the backward pass 140 cycles a chunk, whether it looks or not.)
+__device__ __forceinline__ void publish(int& top, uint32_t taddr, float d, int lane) {
+    uint32_t f[32];
+    tc::ld32(taddr, f);
+    tc::wait_ld();
     __half2 m[2] = {__float2half2_rn(0.0f), __float2half2_rn(0.0f)};
 #pragma unroll
-    for (int i = 0; i < 32; ++i) m[i & 1] = __hmax2(m[i & 1], __habs2(*reinterpret_cast<const __half2*>(&f[i >> 4][i & 15])));
+    for (int i = 0; i < 32; ++i) m[i & 1] = __hmax2(m[i & 1], __habs2(*reinterpret_cast<const __half2*>(&f[i])));
     const float2 y = __half22float2(__hmax2(m[0], m[1]));
     publish(top, d * fmaxf(y.x, y.y), lane);
 }
