@@ -217,6 +217,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1) gdr_bwd_chunk_kernel(GdrBack
     fetch_gates(now, now.hk * share + rank, 0);
     fetch_first(now, now.hk * share + rank);
     fetch_second(now, now.hk * share + rank);
+    // the exponents of S and X, and of dO, dS and Y: fetched a head ahead
+    const auto scales_of = [&](const Place& p, int h) {
+        return *reinterpret_cast<const int2*>(P.blocks + ((size_t)p.chunk * I.Hv + h) * kBlockBytes + 2 * kTileBytes + 4 * kGateScale);
+    };
+    int2 scales = scales_of(now, now.hk * share + rank);
     float dq[4][4], dk[4][4], kk[2][4];
     for (bool more = true; more; now = next, kq ^= 1) {
         pair += gridDim.x;
@@ -259,10 +264,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) gdr_bwd_chunk_kernel(GdrBack
 #pragma unroll
                 for (int m = 0; m < 4; ++m)
                     v[i][m] = (m & 1 ? i1 : i0) < rows ? __ldg(reinterpret_cast<const uint32_t*>(vp + (m & 1 ? 8 * I.v_stride : 0) + 16 * i + 8 * (m >> 1))) : 0u;
-            // the exponents of S and X, and of dO, dS and Y
-            const int* scales = reinterpret_cast<const int*>(P.blocks + ((size_t)now.chunk * I.Hv + h) * kBlockBytes + 2 * kTileBytes);
-            const int held = scales[kGateScale] + scales[kGateGradScale];
-            const float by = I.scale * power_of_two(scales[kGateGradScale]);
+            const int held = scales.x + scales.y;
+            const float by = I.scale * power_of_two(scales.y);
             if (h == h0) unit = held;
             else if (held < unit) lower_unit(held);
             const float f = power_of_two(unit - held);
@@ -274,6 +277,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) gdr_bwd_chunk_kernel(GdrBack
             }
             __syncthreads();
             if (follows) {
+                scales = scales_of(then, then_h);
                 prefetch(then, then_h);
                 fetch_gates(then, then_h, turn ^ 1);
                 if (last) fetch_pair(next, kq ^ 1);

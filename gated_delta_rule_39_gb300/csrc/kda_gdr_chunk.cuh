@@ -38,6 +38,7 @@ constexpr int kC = 64;                        // tokens per chunk
 constexpr int kTileBytes = kC * kC * 2;
 constexpr int kGateB = 0, kGateBe = kC, kGateE = 2 * kC, kGateEnd = 3 * kC, kGateG = 4 * kC, kGateAll = 5 * kC;
 constexpr int kGateDo = kGateAll + 1, kGateScale = kGateAll + 2, kGateGradScale = kGateAll + 3;
+static_assert(kGateScale % 2 == 0 && kGateGradScale == kGateScale + 1, "one access");
 constexpr int kGateFloats = kGateAll + 4;
 constexpr int kBlockUsed = 2 * kTileBytes + kGateFloats * 4;   // 17,680
 constexpr int kBlockBytes = (kBlockUsed + 127) / 128 * 128;
