@@ -28,7 +28,7 @@
 // same chain with mma.sync and a warp per 16 channels took 645).  Of some 3,100 cycles the tensor core runs
 // 1,200; the rest are the three roundings (100 to 350 cycles each), the hand-overs (130 to 190
 // cycles from a warp's arrival to the MMA, as many back) and their contention
-// with the other roles (0.47 of the issue slots are taken).
+// with the other roles (0.49 of the issue slots are taken).
 // All waits are bounded: a role whose wait gives up returns, and so do those that wait for it.
 #pragma once
 
