@@ -22,8 +22,9 @@
 // Warps: 8 state warps (lane quarter w % 4, half of the columns each) do that rounding; one
 // warp issues the MMAs, those that the chain does not need behind the state's update;
 // 4 warps bring in keys, values, T and P of the next chunks, 4 the queries, 4 write the
-// outputs, one chooses the scales and two find out how large the values are.  Every role's loop is kept small: with the MMAs issued from a state warp, the
-// others' jumps over that code cost 200 cycles each (instruction cache misses).
+// outputs, one chooses the scales and two find out how large the values are.  Every role's loop is
+// kept small: with the MMAs issued from a state warp, the others' jumps over that code cost 200 cycles
+// each (instruction cache misses).
 // Measured: 1.65 us per chunk of 64 tokens (8,192 tokens x 96 heads on 96 SMs: 213 us, 204 with scales left out; the
 // same chain with mma.sync and a warp per 16 channels took 645).  Of some 3,100 cycles the tensor core runs
 // 1,200; the rest are the three roundings (100 to 350 cycles each), the hand-overs (130 to 190
